@@ -1,0 +1,125 @@
+/*
+ * w4a4_ops.h -- operators beside the W4A4 layer, in the same library (libw4a4): the layer's 4-bit
+ * weights for single tokens, layer normalisation, activations kept in 8 bits and the gated
+ * feed-forward block, with their gradients. Conventions (ownership, bf16 as uint16_t, errors, streams) are
+ * those of w4a4.h; device pointers must be 16-byte aligned where nothing else is said. Calls keep no state
+ * and share no memory: a call's scratch is the caller's `ws`, which it may use again for the next call on the
+ * same stream. Every call may be captured into a graph. Non-finite inputs: as in the formulas (Inf and NaN
+ * propagate within what they enter), never an access out of bounds.
+ */
+#ifndef W4A4_OPS_H
+#define W4A4_OPS_H
+
+#include "w4a4.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define W4A4_MATVEC_MAX_ROWS 16  /* rows of X of w4a4_matvec */
+#define W4A4_CHECKPOINT_BLOCK 32 /* tokens that share a scale in an 8-bit checkpoint */
+
+typedef enum {               /* element types */
+  W4A4_DTYPE_BF16 = 0,
+  W4A4_DTYPE_F32 = 1
+} w4a4_dtype_t;
+
+typedef enum {               /* activations of the gated feed-forward block */
+  W4A4_ACT_SILU = 0,         /* g / (1 + exp(-g)) */
+  W4A4_ACT_GELU = 1          /* (g / 2)(1 + erf(g / sqrt 2)) */
+} w4a4_act_t;
+
+/* ------------------------------- the layer for single tokens (device, asynchronous on `stream`) */
+
+/*
+ * Weight-only form of the layer for 1 <= M <= W4A4_MATVEC_MAX_ROWS rows: the 4-bit weights of a
+ * prepared layer against activations that are not quantized,
+ *   Y[m][n] = bf16( sum_k X^[m][k] deq(Q)[n][k] + sum_i t[m][i] L2[i][n] + bias[n] ),
+ *   X^ = fp32(X · inv_lambda) taken as the sum of two bf16 numbers, t = X^·L1, fp32 accumulation.
+ * fmt INT4 (group 64) or MXFP4 (block 32); W4A4_ERR_UNSUPPORTED for W8A8. Shapes as
+ * w4a4_buffer_sizes.
+ *
+ * w4a4_matvec_sizes: bytes of the weights in this call's layout (wv, laid out once) and of the
+ * workspace of one call (ws). Calls that overlap in time need a workspace each.
+ *
+ * w4a4_matvec_weights: canonical codes [N][K/2] and scales (INT4 [N][K/64] bf16, MXFP4 [N][K/32] E8M0
+ * bytes; w4a4_codes_to_canonical / w4a4_scales_to_canonical give them), both device -> wv (device).
+ *
+ * w4a4_matvec: X [M][ldx] bf16 (ldx as w4a4_quantize_act), inv_lambda [K] fp32, l1t [rank_pad][K],
+ * l2t [n_pad][rank_pad] in library layout (NULL allowed when rank == 0), bias [N] bf16 or NULL,
+ * Y [M][ldy] bf16, ldy >= N, any alignment of 2 bytes.
+ */
+w4a4_status_t w4a4_matvec_sizes(int M, int N, int K, int rank, int fmt, size_t* wv, size_t* ws);
+w4a4_status_t w4a4_matvec_weights(const uint8_t* codes, const void* scales, int N, int K, int fmt, uint8_t* wv,
+                                  w4a4_stream_t stream);
+w4a4_status_t w4a4_matvec(const uint16_t* X, int M, int K, int ldx, const float* inv_lambda, const uint16_t* l1t,
+                          const uint8_t* wv, const uint16_t* l2t, const uint16_t* bias, uint16_t* Y, int ldy, int N,
+                          int rank, int fmt, void* ws, w4a4_stream_t stream);
+
+/* ------------------------------------------ training calls (device, asynchronous on `stream`) */
+
+/*
+ * Layer normalisation over the K elements of each row and its gradients, any M, K >= 1 (M <= 2^30,
+ * K <= 2^26) and row strides >= K:
+ *   mean = sum(x)/K, rstd = 1/sqrt(sum((x - mean)^2)/K + eps), y = (x - mean) rstd gamma + beta;
+ *   with h = (x - mean) rstd, d = dy gamma: dx = rstd (d - mean(d) - h mean(d h)),
+ *   dgamma = sum over rows of dy h, dbeta = sum over rows of dy.
+ *   X, Y, dY, dX  of `dtype`; gamma, beta [K] of `param_dtype` (NULL: 1 and 0); every tensor aligned to
+ *                 its elements; mean, rstd [M] and dgamma, dbeta [K] fp32 (either gradient may be NULL).
+ *                 Statistics and sums in fp32; outputs must not overlap inputs. eps >= 0.
+ *   ws            w4a4_layer_norm_backward_bytes(M, K) bytes (0 for a shape out of range); needed only
+ *                 where dgamma or dbeta is not NULL. The gradients do not depend on timing.
+ */
+w4a4_status_t w4a4_layer_norm(const void* X, int M, int K, int ldx, int dtype, const void* gamma, const void* beta,
+                              int param_dtype, float eps, void* Y, int ldy, float* mean, float* rstd,
+                              w4a4_stream_t stream);
+size_t w4a4_layer_norm_backward_bytes(int M, int K);
+w4a4_status_t w4a4_layer_norm_backward(const void* dY, int lddy, const void* X, int ldx, int dtype, const void* gamma,
+                                       int param_dtype, const float* mean, const float* rstd, int M, int K, void* dX,
+                                       int lddx, float* dgamma, float* dbeta, void* ws, w4a4_stream_t stream);
+
+/*
+ * Activations kept in 8 bits for the backward pass, X [M][ldx] bf16, K a multiple of 8, ldx >= K a
+ * multiple of 8. Per channel and block of W4A4_CHECKPOINT_BLOCK tokens, with a = max |x| of the block:
+ *   e = min{e >= -127 : 127 2^e >= a}, q = rint(x 2^-e), read back as x~ = q 2^e (a bf16 number;
+ *   |q| <= 63 at e = 122, the largest e, so that no finite block reads back as Inf).
+ *   codes  [ceil(M/32)][K][32] int8, the 32 tokens of a channel together, 0 for tokens past M
+ *   scales [ceil(M/32)][K] bytes e + 127; 255 for a block that holds an Inf or NaN, which reads back
+ *          as NaN throughout
+ * w4a4_checkpoint_sizes gives the bytes of both.
+ *
+ * w4a4_checkpoint_weight_grad: dW [N][K] = dY^T·X~ (dY [M][lddy] bf16, N a multiple of 8, lddy >= N a
+ * multiple of 8), fp32 accumulation; dW of `out_dtype`, contiguous. ws:
+ * w4a4_checkpoint_weight_grad_bytes(M, N, K) bytes (0 for a shape out of range).
+ */
+w4a4_status_t w4a4_checkpoint_sizes(int M, int K, size_t* codes, size_t* scales);
+w4a4_status_t w4a4_checkpoint_pack(const uint16_t* X, int M, int K, int ldx, int8_t* codes, uint8_t* scales,
+                                   w4a4_stream_t stream);
+w4a4_status_t w4a4_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, int M, int K, uint16_t* X, int ldx,
+                                     w4a4_stream_t stream);
+size_t w4a4_checkpoint_weight_grad_bytes(int M, int N, int K);
+w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const int8_t* codes, const uint8_t* scales, int M,
+                                          int N, int K, void* dW, int out_dtype, void* ws, w4a4_stream_t stream);
+
+/*
+ * The gated feed-forward block's first half and its gradients, bf16 with fp32 accumulation:
+ *   G = X·Wg^T, U = X·Wu^T, H = bf16(act(G) U)
+ *   dG = bf16(dH U act'(G)), dU = bf16(dH act(G)), dX = dG·Wg + dU·Wu, dWg = dG^T·X, dWu = dU^T·X.
+ *   X [M][ldx], Wg and Wu [F][ldw], H and dH [M][ld >= F]; K and F multiples of 8, row strides multiples
+ *   of 8 up to 2^21; dX [M][K], dWg and dWu [F][K] contiguous. G and U are computed again in the backward
+ *   pass (they are not kept). M >= 1; up to 16 rows the forward pass has a kernel for single tokens.
+ *   ws   w4a4_gated_forward_bytes / w4a4_gated_backward_bytes (M, K, F) bytes (may be NULL where 0).
+ * W4A4_ERR_UNSUPPORTED for an unknown act.
+ */
+size_t w4a4_gated_forward_bytes(int M, int K, int F);
+w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg, const uint16_t* Wu, int ldw,
+                                 int F, int act, uint16_t* H, int ldh, void* ws, w4a4_stream_t stream);
+size_t w4a4_gated_backward_bytes(int M, int K, int F);
+w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg,
+                                  const uint16_t* Wu, int ldw, int F, int act, uint16_t* dX, uint16_t* dWg, uint16_t* dWu,
+                                  void* ws, w4a4_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* W4A4_OPS_H */

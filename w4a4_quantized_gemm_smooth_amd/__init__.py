@@ -23,7 +23,10 @@ __all__ = [
     "buffer_sizes", "column_absmax", "smooth_factors", "prepare_weights", "append_lowrank",
     "codes_to_canonical", "scales_to_canonical", "quantize_act", "lowrank_linear", "W4A4Linear",
     "FMT_W8A8", "gelu_quantize_act", "lowrank_linear_gelu_quant", "gelu_quant_xl1_bytes", "MLPPair",
-    "lowrank_linear_gelu_quant_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "lowrank_linear_gelu_quant_noalloc", "NOALLOC_SCRATCH_BYTES", "MATVEC_MAX_ROWS", "CHECKPOINT_BLOCK", "matvec_sizes",
+    "matvec_weights", "matvec", "layer_norm", "layer_norm_backward", "layer_norm_backward_bytes", "checkpoint_sizes",
+    "checkpoint_pack", "checkpoint_unpack", "checkpoint_weight_grad", "checkpoint_weight_grad_bytes", "gated_forward",
+    "gated_forward_bytes", "gated_backward", "gated_backward_bytes",
 ]
 
 FMT_INT4_G64 = 0
@@ -36,6 +39,9 @@ RANK_ALIGN = 16
 MAX_RANK = 128
 W8A8_MAX_K = 131072
 NOALLOC_SCRATCH_BYTES = 32 << 20
+MATVEC_MAX_ROWS = 16
+CHECKPOINT_BLOCK = 32
+_ACTS = {"silu": 0, "gelu": 1}
 _FMT_NAMES = {"int4_g64": FMT_INT4_G64, "mxfp4_b32": FMT_MXFP4_B32, "w8a8": FMT_W8A8}
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -88,6 +94,24 @@ def lib() -> ctypes.CDLL:
             "w4a4_lowrank_linear_gelu_quant": [P, P, P, P, P, P, P, I, I, I, I, I, P, P, I, P, P, P, P, I, P],
             "w4a4_lowrank_linear_gelu_quant_noalloc": [P, P, P, P, P, P, P, I, I, I, I, I, P, P, I, P, P, P, P, I, P],
         }
+        SP = ctypes.POINTER(ctypes.c_size_t)
+        sigs.update({
+            "w4a4_matvec_sizes": [I, I, I, I, I, SP, SP],
+            "w4a4_matvec_weights": [P, P, I, I, I, P, P],
+            "w4a4_matvec": [P, I, I, I, P, P, P, P, P, P, I, I, I, I, P, P],
+            "w4a4_layer_norm": [P, I, I, I, I, P, P, I, F, P, I, P, P, P],
+            "w4a4_layer_norm_backward": [P, I, P, I, I, P, I, P, P, I, I, P, I, P, P, P, P],
+            "w4a4_checkpoint_sizes": [I, I, SP, SP],
+            "w4a4_checkpoint_pack": [P, I, I, I, P, P, P],
+            "w4a4_checkpoint_unpack": [P, P, I, I, P, I, P],
+            "w4a4_checkpoint_weight_grad": [P, I, P, P, I, I, I, P, I, P, P],
+            "w4a4_gated_forward": [P, I, I, I, P, P, I, I, I, P, I, P, P],
+            "w4a4_gated_backward": [P, I, P, I, I, I, P, P, I, I, I, P, P, P, P, P],
+        })
+        for name in ("w4a4_layer_norm_backward_bytes", "w4a4_checkpoint_weight_grad_bytes", "w4a4_gated_forward_bytes",
+                     "w4a4_gated_backward_bytes"):
+            getattr(L, name).argtypes = [I, I] if name == "w4a4_layer_norm_backward_bytes" else [I, I, I]
+            getattr(L, name).restype = S
         for name, args in sigs.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -365,6 +389,235 @@ def gelu_quant_xl1_bytes(M: int, N: int, rank2: int) -> int:
     return int(lib().w4a4_gelu_quant_xl1_bytes(M, N, rank2))
 
 
+# ------------------------------------------------------------- single tokens and training calls
+def _check_tensor(name, t, dtype, shape, device, contiguous=True):
+    """A tensor of a given type and shape on ``device``: contiguous, or a matrix of any row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif shape[1] > 1 and t.stride(1) != 1 or shape[0] > 1 and t.stride(0) < shape[1]:
+        raise ValueError(f"{name} must have unit stride along its last dimension and rows that do not overlap")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a GPU'} (got {t.device})")
+
+
+def _ld(t):
+    """Row stride of a matrix; torch leaves the stride of a single row free, then its width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _matrix_shape(name, t):
+    if getattr(t, "ndim", 0) != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape
+
+
+def _two_sizes(fn, *args):
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(fn, getattr(lib(), fn)(*args, ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def matvec_sizes(M: int, N: int, K: int, rank: int, fmt=FMT_INT4_G64) -> dict:
+    """Bytes of ``matvec``'s weights (``wv``, laid out once) and of the workspace of one call (``ws``)."""
+    wv, ws = _two_sizes("w4a4_matvec_sizes", M, N, K, rank, _fmt(fmt))
+    return dict(wv=wv, ws=ws)
+
+
+def matvec_weights(codes, scales, N, K, fmt, wv, stream=None):
+    """Lay canonical codes [N, K/2] (uint8) and scales (INT4: [N, K/64] bf16; MXFP4: [N, K/32] uint8) out
+    as ``matvec`` reads them; all on the GPU."""
+    import torch
+    f = _fmt(fmt)
+    dev = getattr(wv, "device", torch.device("cpu"))
+    _check_tensor("codes", codes, torch.uint8, (N, K // 2), dev)
+    if f == FMT_INT4_G64:
+        _check_tensor("scales", scales, torch.bfloat16, (N, K // GROUP), dev)
+    else:
+        _check_tensor("scales", scales, torch.uint8, (N, K // MX_BLOCK), dev)
+    _check_buffer("wv", wv, matvec_sizes(1, N, K, 0, f)["wv"], dev)
+    _check("w4a4_matvec_weights", lib().w4a4_matvec_weights(_dptr(codes), _dptr(scales), N, K, f, _dptr(wv), _stream(stream)))
+
+
+def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=None):
+    """The layer for up to 16 rows of x [M, K] bf16 without quantizing them: y [M, N] bf16 (weight-only
+    4-bit products, the low-rank branch and the bias; two kernels). ``wv`` from ``matvec_weights``."""
+    import torch
+    f = _fmt(fmt)
+    M = _matrix_shape("x", x)[0]
+    dev = x.device
+    wv_bytes, ws_bytes = _two_sizes("w4a4_matvec_sizes", M, N, K, rank, f)
+    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
+    _check_tensor("y", y, torch.bfloat16, (M, N), dev, False)
+    rp = (rank + RANK_ALIGN - 1) // RANK_ALIGN * RANK_ALIGN
+    for name, t, n in (("inv_lambda", inv_lambda, 4 * K), ("wv", wv, wv_bytes), ("ws", ws, ws_bytes), ("l1t", l1t, 2 * rp * K),
+                       ("l2t", l2t, 2 * rp * N), ("bias", bias, 0 if bias is None else 2 * N)):
+        _check_buffer(name, t, n, dev)
+    _check("w4a4_matvec", lib().w4a4_matvec(
+        _dptr(x), M, K, _ld(x), _dptr(inv_lambda), _dptr(l1t), _dptr(wv), _dptr(l2t), _dptr(bias), _dptr(y), _ld(y), N, rank, f,
+        _dptr(ws), _stream(stream)))
+
+
+def _dtype(t, name):
+    import torch
+    if t is None or t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return 1
+
+
+def _norm_params(gamma, beta, K, dev):
+    p = gamma if gamma is not None else beta
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _check_tensor(name, t, p.dtype, (K,), dev)
+    return _dtype(p, "gamma and beta")
+
+
+def layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=None):
+    """y = (x - mean) rstd gamma + beta over the rows of x [M, K] (bf16 or fp32; gamma, beta [K] bf16, fp32
+    or None), with the rows' mean and rstd [M] fp32 for ``layer_norm_backward``."""
+    import torch
+    M, K = _matrix_shape("x", x)
+    dev, dt = x.device, _dtype(x, "x")
+    _check_tensor("x", x, x.dtype, (M, K), dev, False)
+    _check_tensor("y", y, x.dtype, (M, K), dev, False)
+    _check_tensor("mean", mean, torch.float32, (M,), dev)
+    _check_tensor("rstd", rstd, torch.float32, (M,), dev)
+    pt = _norm_params(gamma, beta, K, dev)
+    _check("w4a4_layer_norm", lib().w4a4_layer_norm(
+        _dptr(x), M, K, _ld(x), dt, _dptr(gamma), _dptr(beta), pt, eps, _dptr(y), _ld(y), _dptr(mean), _dptr(rstd),
+        _stream(stream)))
+
+
+def layer_norm_backward_bytes(M: int, K: int) -> int:
+    return int(lib().w4a4_layer_norm_backward_bytes(M, K))
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
+    """dx, and dgamma, dbeta [K] fp32 (either may be None; ``ws`` may be None where both are), of
+    ``layer_norm`` from dy, x and the forward pass's mean and rstd."""
+    import torch
+    M, K = _matrix_shape("x", x)
+    dev, dt = x.device, _dtype(x, "x")
+    for name, t in (("dy", dy), ("x", x), ("dx", dx)):
+        _check_tensor(name, t, x.dtype, (M, K), dev, False)
+    _check_tensor("mean", mean, torch.float32, (M,), dev)
+    _check_tensor("rstd", rstd, torch.float32, (M,), dev)
+    for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
+        if t is not None:
+            _check_tensor(name, t, torch.float32, (K,), dev)
+    pt = _norm_params(gamma, None, K, dev)
+    _check_buffer("ws", ws, 0 if dgamma is None and dbeta is None else layer_norm_backward_bytes(M, K), dev)
+    _check("w4a4_layer_norm_backward", lib().w4a4_layer_norm_backward(
+        _dptr(dy), _ld(dy), _dptr(x), _ld(x), dt, _dptr(gamma), pt, _dptr(mean), _dptr(rstd), M, K, _dptr(dx), _ld(dx),
+        _dptr(dgamma), _dptr(dbeta), _dptr(ws), _stream(stream)))
+
+
+def checkpoint_sizes(M: int, K: int) -> dict:
+    """Bytes of the 8-bit codes and of the scales that keep activations [M, K]."""
+    codes, scales = _two_sizes("w4a4_checkpoint_sizes", M, K)
+    return dict(codes=codes, scales=scales)
+
+
+def _check_checkpoint(codes, scales, M, K, dev):
+    c, s = _two_sizes("w4a4_checkpoint_sizes", M, K)
+    _check_buffer("codes", codes, c, dev)
+    _check_buffer("scales", scales, s, dev)
+
+
+def checkpoint_pack(x, codes, scales, stream=None):
+    """Keep x [M, K] bf16 in 8 bits: int8 codes and a power-of-two scale per channel and 32 tokens."""
+    import torch
+    M, K = _matrix_shape("x", x)
+    _check_tensor("x", x, torch.bfloat16, (M, K), x.device, False)
+    _check_checkpoint(codes, scales, M, K, x.device)
+    _check("w4a4_checkpoint_pack", lib().w4a4_checkpoint_pack(
+        _dptr(x), M, K, _ld(x), _dptr(codes), _dptr(scales), _stream(stream)))
+
+
+def checkpoint_unpack(codes, scales, x, stream=None):
+    """What the codes and scales stand for, into x [M, K] bf16 (exact)."""
+    import torch
+    M, K = _matrix_shape("x", x)
+    _check_tensor("x", x, torch.bfloat16, (M, K), x.device, False)
+    _check_checkpoint(codes, scales, M, K, x.device)
+    _check("w4a4_checkpoint_unpack", lib().w4a4_checkpoint_unpack(
+        _dptr(codes), _dptr(scales), M, K, _dptr(x), _ld(x), _stream(stream)))
+
+
+def checkpoint_weight_grad_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().w4a4_checkpoint_weight_grad_bytes(M, N, K))
+
+
+def checkpoint_weight_grad(dy, codes, scales, K, dw, ws, stream=None):
+    """dw [N, K] (fp32 or bf16) = dy^T x for dy [M, N] bf16 and the activations [M, K] kept in (codes,
+    scales)."""
+    import torch
+    M, N = _matrix_shape("dy", dy)
+    dev = dy.device
+    _check_tensor("dy", dy, torch.bfloat16, (M, N), dev, False)
+    _check_checkpoint(codes, scales, M, K, dev)
+    dt = _dtype(dw, "dw")
+    _check_tensor("dw", dw, dw.dtype, (N, K), dev)
+    _check_buffer("ws", ws, checkpoint_weight_grad_bytes(M, N, K), dev)
+    _check("w4a4_checkpoint_weight_grad", lib().w4a4_checkpoint_weight_grad(
+        _dptr(dy), _ld(dy), _dptr(codes), _dptr(scales), M, N, K, _dptr(dw), dt, _dptr(ws), _stream(stream)))
+
+
+def _act(act) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)} (got {act!r})")
+    return _ACTS[act]
+
+
+def _check_gated(x, wg, wu, h, name):
+    import torch
+    M, K = _matrix_shape("x", x)
+    F = _matrix_shape("wg", wg)[0]
+    for n, t, shape in (("x", x, (M, K)), ("wg", wg, (F, K)), ("wu", wu, (F, K)), (name, h, (M, F))):
+        _check_tensor(n, t, torch.bfloat16, shape, x.device, False)
+    if _ld(wg) != _ld(wu):
+        raise ValueError("wg and wu must have the same row stride")
+    return M, K, F
+
+
+def gated_forward_bytes(M: int, K: int, F: int) -> int:
+    return int(lib().w4a4_gated_forward_bytes(M, K, F))
+
+
+def gated_forward(x, wg, wu, act, h, ws=None, stream=None):
+    """h [M, F] = act(x wg^T) * (x wu^T) for x [M, K], wg and wu [F, K], bf16; act "silu" or "gelu"."""
+    M, K, F = _check_gated(x, wg, wu, h, "h")
+    _check_buffer("ws", ws, gated_forward_bytes(M, K, F), x.device)
+    _check("w4a4_gated_forward", lib().w4a4_gated_forward(
+        _dptr(x), M, K, _ld(x), _dptr(wg), _dptr(wu), _ld(wg), F, _act(act), _dptr(h), _ld(h), _dptr(ws), _stream(stream)))
+
+
+def gated_backward_bytes(M: int, K: int, F: int) -> int:
+    return int(lib().w4a4_gated_backward_bytes(M, K, F))
+
+
+def gated_backward(dh, x, wg, wu, act, dx, dwg, dwu, ws, stream=None):
+    """dx [M, K], dwg and dwu [F, K] (bf16) of ``gated_forward`` from dh [M, F] and its inputs."""
+    import torch
+    M, K, F = _check_gated(x, wg, wu, dh, "dh")
+    for n, t, shape in (("dx", dx, (M, K)), ("dwg", dwg, (F, K)), ("dwu", dwu, (F, K))):
+        _check_tensor(n, t, torch.bfloat16, shape, x.device)
+    _check_buffer("ws", ws, gated_backward_bytes(M, K, F), x.device)
+    _check("w4a4_gated_backward", lib().w4a4_gated_backward(
+        _dptr(dh), _ld(dh), _dptr(x), M, K, _ld(x), _dptr(wg), _dptr(wu), _ld(wg), F, _act(act), _dptr(dx), _dptr(dwg),
+        _dptr(dwu), _dptr(ws), _stream(stream)))
+
+
 class W4A4Linear:
     """A prepared layer resident in HBM: codes, scales and low-rank factors of one weight.
 
@@ -384,6 +637,7 @@ class W4A4Linear:
         self.bias = None if bias_bits is None else up(np.asarray(bias_bits, np.uint16), np.int16)
         self.device = self.wq.device   # with its index ("cuda" -> "cuda:0")
         self._act = {}
+        self._wv, self._ws = None, {}
 
     @classmethod
     def from_weights(cls, w_bits, lam, inv_lambda, rank, fmt=FMT_INT4_G64, l1_bits=None, l2_bits=None, **kw):
@@ -418,6 +672,43 @@ class W4A4Linear:
             y = torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
         a = self.quantize(x, stream)
         return self.gemm(a, M, y, stream)
+
+
+    def token_weights(self):
+        """The weights as ``matvec`` reads them, laid out from the layer's codes and scales on first use."""
+        import torch
+        if self._wv is None:
+            N, K, f = self.N, self.K, self.fmt
+            codes = codes_to_canonical(self.wq.cpu().numpy(), N, K, f)
+            scales = scales_to_canonical(self.wscale.cpu().numpy(), N, K, f)
+            codes = torch.from_numpy(codes).to(self.device)
+            if f == FMT_INT4_G64:
+                scales = torch.from_numpy(scales.view(np.int16)).to(self.device).view(torch.bfloat16)
+            else:
+                scales = torch.from_numpy(scales).to(self.device)
+            wv = torch.empty(matvec_sizes(1, N, K, 0, f)["wv"], dtype=torch.uint8, device=self.device)
+            with torch.cuda.device(self.device):
+                matvec_weights(codes, scales, N, K, f, wv)
+                torch.cuda.current_stream().synchronize()   # calls on any stream find it complete
+            self._wv = wv
+        return self._wv
+
+    def tokens(self, x, y=None, stream=None):
+        """y [M, N] for 1 to 16 rows of x [M, K] bf16, activations not quantized (``matvec``; INT4 and MXFP4
+        layers). The workspace is kept per M, so calls that overlap in time on several streams need a layer
+        object each."""
+        import torch
+        M = x.shape[0]
+        if len(x.shape) != 2 or x.shape[1] != self.K or not 1 <= M <= MATVEC_MAX_ROWS:
+            raise ValueError(f"x has shape {tuple(x.shape)}, needs [1 to {MATVEC_MAX_ROWS}, {self.K}]")
+        if y is None:
+            y = torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
+        if M not in self._ws:
+            n = matvec_sizes(M, self.N, self.K, self.rank, self.fmt)["ws"]
+            self._ws[M] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        matvec(x, self.inv_lambda, self.l1t, self.token_weights(), self.l2t, self.bias, y, self.N, self.K, self.rank, self.fmt,
+               self._ws[M], stream)
+        return y
 
 
 class MLPPair:

@@ -1,0 +1,150 @@
+// Activations kept in 8 bits for the backward pass. A block is 32 consecutive tokens of one channel;
+// with a = max |x| over it,
+//     e = min{e >= -127 : 127 2^e >= a},   q = rint(x 2^-e)  (|q| <= 127),   x~ = q 2^e
+// (|q| <= 63 at the largest e, 122, which only the largest bf16 number needs: 64 2^122 is no number).
+// The scale runs along the tokens because the outliers that smoothing deals with sit in a few channels:
+// they then cost their neighbours nothing. It is a power of two, so x~ has at most 7 significant bits
+// and is a bf16 number: reading the codes back, or feeding them to a bf16 matrix product, rounds
+// nothing.
+//
+// Layout: codes [ceil(M/32)][K][32] int8 (the 32 tokens of a channel together: a weight gradient's
+// contraction runs along them, so its matrix operand is 8 consecutive bytes), scales [ceil(M/32)][K]
+// bytes e + 127; 255 marks a block that holds an Inf or NaN, whose values all read back as NaN.
+//
+// Both kernels move each byte once; a thread owns 4 channels of a block: 32 loads (or stores) of 8
+// bytes down the tokens, one 128-byte line of codes.
+#include "w4a4_device_common.h"
+
+using namespace w4a4;
+using namespace w4a4::dev;
+
+namespace {
+
+constexpr int CK_CH = 4;        // channels per thread
+constexpr int CK_THREADS = 256;
+
+__device__ __forceinline__ float half_of(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16)); }
+
+// 2^e from its byte; byte 0 is the subnormal 2^-127, 255 NaN
+__device__ __forceinline__ float e8m0(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7FC00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
+
+__global__ __launch_bounds__(CK_THREADS) void checkpoint_pack_kernel(const uint16_t* __restrict__ X, int M, int K, int ldx,
+                                                                     int8_t* __restrict__ codes,
+                                                                     uint8_t* __restrict__ scales) {
+  const int nk = (K + CK_CH * CK_THREADS - 1) / (CK_CH * CK_THREADS), b = blockIdx.x / nk;
+  const int k = (blockIdx.x % nk * CK_THREADS + threadIdx.x) * CK_CH;
+  if (k >= K) return;
+  const int rows = min(W4A4_CHECKPOINT_BLOCK, M - b * W4A4_CHECKPOINT_BLOCK);
+  const uint16_t* x = X + (size_t)b * W4A4_CHECKPOINT_BLOCK * ldx + k;
+  uint2 v[W4A4_CHECKPOINT_BLOCK];
+#pragma unroll
+  for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r)
+    v[r] = r < rows ? *reinterpret_cast<const uint2*>(x + (size_t)r * ldx) : uint2{0u, 0u};
+  uint32_t bytes = 0u;
+  uint4* out = reinterpret_cast<uint4*>(codes + ((size_t)b * K + k) * W4A4_CHECKPOINT_BLOCK);
+#pragma unroll
+  for (int c = 0; c < CK_CH; ++c) {
+    uint32_t top = 0u;   // the largest magnitude's bits (magnitudes order as their bits do, NaN last)
+#pragma unroll
+    for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r)
+      top = max(top, ((c < 2 ? v[r].x : v[r].y) >> (16 * (c & 1))) & 0x7FFFu);
+    // a = 1.m 2^(t-127): 127 2^e >= a from e = t - 133 on where 1.m <= 127/64 (m <= 126 of 128)
+    const int t = (int)(top >> 7), e = max(0, t - 6 + ((top & 127u) > 126u ? 1 : 0));
+    const bool bad = t == 255;
+    bytes |= (uint32_t)(bad ? 255 : e) << (8 * c);
+    const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);   // 2^-(e - 127); e <= 249
+    const float most = e == 249 ? 63.f : 127.f;
+    uint32_t w[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      uint32_t word = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * d + i;
+        const float y = fminf(most, fmaxf(-most, __builtin_rintf(half_of(c < 2 ? v[r].x : v[r].y, c & 1) * inv)));
+        word |= ((uint32_t)(bad ? 0 : (int)y) & 0xFFu) << (8 * i);
+      }
+      w[d] = word;
+    }
+    out[2 * c] = uint4{w[0], w[1], w[2], w[3]};
+    out[2 * c + 1] = uint4{w[4], w[5], w[6], w[7]};
+  }
+  *reinterpret_cast<uint32_t*>(scales + (size_t)b * K + k) = bytes;
+}
+
+__global__ __launch_bounds__(CK_THREADS) void checkpoint_unpack_kernel(const int8_t* __restrict__ codes,
+                                                                       const uint8_t* __restrict__ scales, int M, int K,
+                                                                       uint16_t* __restrict__ X, int ldx) {
+  const int nk = (K + CK_CH * CK_THREADS - 1) / (CK_CH * CK_THREADS), b = blockIdx.x / nk;
+  const int k = (blockIdx.x % nk * CK_THREADS + threadIdx.x) * CK_CH;
+  if (k >= K) return;
+  const int rows = min(W4A4_CHECKPOINT_BLOCK, M - b * W4A4_CHECKPOINT_BLOCK);
+  uint16_t* x = X + (size_t)b * W4A4_CHECKPOINT_BLOCK * ldx + k;
+  const uint4* in = reinterpret_cast<const uint4*>(codes + ((size_t)b * K + k) * W4A4_CHECKPOINT_BLOCK);
+  uint4 q[2 * CK_CH];
+#pragma unroll
+  for (int i = 0; i < 2 * CK_CH; ++i) q[i] = in[i];
+  const uint32_t bytes = *reinterpret_cast<const uint32_t*>(scales + (size_t)b * K + k);
+  float s[CK_CH];
+#pragma unroll
+  for (int c = 0; c < CK_CH; ++c) s[c] = e8m0((bytes >> (8 * c)) & 255u);
+#pragma unroll
+  for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r) {
+    float f[CK_CH];
+#pragma unroll
+    for (int c = 0; c < CK_CH; ++c) {
+      const uint4 p = q[2 * c + (r >> 4)];
+      const uint32_t w = (r & 12) == 0 ? p.x : (r & 12) == 4 ? p.y : (r & 12) == 8 ? p.z : p.w;
+      f[c] = (float)(int8_t)(w >> (8 * (r & 3))) * s[c];   // exact in bf16
+    }
+    if (r < rows) *reinterpret_cast<uint2*>(x + (size_t)r * ldx) = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  }
+}
+
+unsigned checkpoint_blocks(int M, int K) {
+  return (unsigned)((M + W4A4_CHECKPOINT_BLOCK - 1) / W4A4_CHECKPOINT_BLOCK) *
+         (unsigned)((K + CK_CH * CK_THREADS - 1) / (CK_CH * CK_THREADS));
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+w4a4_status_t check_checkpoint(const void* X, int M, int K, int ldx, const void* codes, const void* scales) {
+  if (!checkpoint_shape_ok(M, K) || ldx < K || ldx % 8 != 0) return W4A4_ERR_INVALID_ARG;
+  if (!X || !codes || !scales || !aligned16(X) || !aligned16(codes) || !aligned(scales, 4)) return W4A4_ERR_INVALID_ARG;
+  return W4A4_OK;
+}
+
+}  // namespace
+
+// ================================================================================ C ABI (device)
+extern "C" {
+
+w4a4_status_t w4a4_checkpoint_sizes(int M, int K, size_t* codes, size_t* scales) {
+  if (!checkpoint_shape_ok(M, K) || !codes || !scales) return W4A4_ERR_INVALID_ARG;
+  const size_t blocks = ((size_t)M + W4A4_CHECKPOINT_BLOCK - 1) / W4A4_CHECKPOINT_BLOCK;
+  *codes = blocks * W4A4_CHECKPOINT_BLOCK * (size_t)K;
+  *scales = blocks * (size_t)K;
+  return W4A4_OK;
+}
+
+w4a4_status_t w4a4_checkpoint_pack(const uint16_t* X, int M, int K, int ldx, int8_t* codes, uint8_t* scales,
+                                   w4a4_stream_t stream) {
+  const w4a4_status_t s = check_checkpoint(X, M, K, ldx, codes, scales);
+  if (s != W4A4_OK) return s;
+  hipLaunchKernelGGL(checkpoint_pack_kernel,
+                     dim3(checkpoint_blocks(M, K)), dim3(CK_THREADS), 0, reinterpret_cast<hipStream_t>(stream), X, M, K, ldx, codes, scales);
+  return hipGetLastError() == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+w4a4_status_t w4a4_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, int M, int K, uint16_t* X, int ldx,
+                                     w4a4_stream_t stream) {
+  const w4a4_status_t s = check_checkpoint(X, M, K, ldx, codes, scales);
+  if (s != W4A4_OK) return s;
+  hipLaunchKernelGGL(checkpoint_unpack_kernel,
+                     dim3(checkpoint_blocks(M, K)), dim3(CK_THREADS), 0, reinterpret_cast<hipStream_t>(stream), codes, scales, M, K, X, ldx);
+  return hipGetLastError() == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+}  // extern "C"

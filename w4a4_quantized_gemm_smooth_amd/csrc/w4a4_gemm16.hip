@@ -1,0 +1,568 @@
+// Training-side matrix products in bf16 with fp32 accumulators: the gated feed-forward block
+//     G = X Wg^T,  U = X Wu^T,  H = act(G) (.) U                          (one kernel)
+// and its gradients
+//     dG = dH (.) U (.) act'(G),  dU = dH (.) act(G)                      (the same kernel's other epilogue)
+//     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,
+// and the weight gradient dW = dY^T X~ from activations kept in 8 bits (w4a4_checkpoint.hip).
+// One row of X at a time (1 to 16 tokens) the forward pass is bound by reading the weights and has a
+// kernel of its own.
+//
+// The product kernel. Blocks of 256 x 256 outputs, eight waves of 128 x 64 (4 x 2 tiles of 32x32, 128
+// accumulators to a lane). A step is 32 of the contraction: 16 KB an operand in one of four ring slots
+// in LDS, copied global -> LDS three steps ahead by the LDS DMA path of waves 0..3. Operands are copied
+// as they lie in memory, whichever of their axes is contiguous:
+//   ROWS   contraction contiguous: LDS row = output row, 64 bytes of contraction; a lane's operand (8 of
+//          the contraction) is one 16-byte read. Chunk c of row r is kept at c ^ ((r >> 2) & 3).
+//   COLS   output axis contiguous: LDS row = one of the contraction, 512 bytes of the output axis; a
+//          lane's operand is two transposing reads (four rows of 16 columns to 16 lanes). Chunk c of
+//          row k is kept at c ^ cols_sw(k), so the rows a read takes together lie in other banks.
+//   CODES  8-bit codes with a scale per column and step (B only): 32 bytes of contraction to a column,
+//          converted after the read; the values are bf16 numbers, so nothing is rounded.
+// Outside its range a copy's address is moved past the buffer's end, which reads as zero, so ragged
+// sizes cost nothing in the loop.
+#include <type_traits>
+
+#include "w4a4_device_common.h"
+
+using namespace w4a4;
+using namespace w4a4::dev;
+
+namespace {
+
+enum : int { ROWS = 0, COLS = 1, CODES = 2 };
+enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_GATED = 2, OUT_GATED_GRAD = 3 };
+
+constexpr int TB = 256;          // block rows and columns
+constexpr int KSTEP = 32;        // contraction per step
+constexpr int NSLOT = 4;         // ring slots
+constexpr int GM_THREADS = 512;
+constexpr int GM_MAX_LD = 1 << 21;   // 256 rows stay below 2^31 bytes
+constexpr int RSRC_W3 = 0x00020000;
+constexpr int OOB = (int)0x80000000;
+
+struct GemmArgs {
+  // A: [0] alone, or per contraction segment (segs = 2), or per problem (probs = 2: two products with
+  // the same B, the block rows of the second following the first's). B: [0] alone, per segment, or
+  // (gated) the two weights whose rows share a block.
+  const void *A[2], *B[2];
+  const uint8_t* scales;           // CODES
+  void* out[2];
+  const uint16_t* dH;              // OUT_GATED_GRAD: [rows][lddh]; out = {dG, dU}
+  int lda, ldb, ldo, lddh;
+  int rows, cols, K;               // per problem; K per segment; gated: cols of one weight
+  int segs, probs, steps;          // steps per segment
+  int splits;                      // parts of the contraction, each to its own plane of out[0] (OUT_F32)
+  int act;
+};
+
+__device__ __forceinline__ int cols_sw(int k, bool perm) { return 2 * ((k & 3) | (((perm ? k >> 4 : k >> 3) & 1) << 2)); }
+
+struct __attribute__((aligned(16))) Slot {
+  uint8_t a[TB * KSTEP * 2];
+  uint8_t b[TB * KSTEP * 2];
+};
+
+__device__ __forceinline__ void act_of(int act, float g, float& a, float& slope) {
+  if (act == W4A4_ACT_SILU) {
+    const float p = 1.0f / (1.0f + __expf(-g));
+    a = g * p;
+    slope = p * (1.0f + g * (1.0f - p));
+  } else {
+    const float p = 0.5f * (1.0f + erff(g * 0.70710678f));
+    a = g * p;
+    slope = p + g * __expf(-0.5f * g * g) * 0.39894228f;
+  }
+}
+
+// The wave's 32-column tiles J0 .. J0 + NT - 1, fp32 -> bf16 through LDS, in whole 16-byte pieces of rows.
+// `stage`: 64 rows of NT * 64 + 16 bytes. cols is a multiple of 8, rows are 16-byte aligned.
+template <int J0, int NT>
+__device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stage, uint16_t* out, int ld, int rows, int cols,
+                                            int r0, int c0, int lane) {
+  constexpr int ES = NT * 64 + 16, CPR = NT * 4;
+  const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; v += 2) {
+          const int rl = ii * 32 + 8 * (v >> 2) + 4 * lh + (v & 3);
+          const uint32_t pr = pack_bf16x2(t[2 * half + ii][J0 + j][v], t[2 * half + ii][J0 + j][v + 1]);
+          uint16_t* d = reinterpret_cast<uint16_t*>(stage + rl * ES + (j * 32 + lr) * 2);
+          d[0] = (uint16_t)pr;
+          d[ES / 2] = (uint16_t)(pr >> 16);
+        }
+#pragma unroll
+    for (int q = 0; q < CPR; ++q) {
+      const int idx = q * 64 + lane, rr = idx / CPR, c = idx % CPR;
+      const uint4 val = *reinterpret_cast<const uint4*>(stage + rr * ES + c * 16);
+      const int row = r0 + half * 64 + rr, col = c0 + c * 8;
+      if (row < rows && col < cols) *reinterpret_cast<uint4*>(out + (size_t)row * ld + col) = val;
+    }
+  }
+}
+
+template <int AM, int BM, int EPI>
+__global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g) {
+  constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
+  constexpr bool PERM = BM == CODES;   // contraction order of a step: 16 h + 8 s + e instead of 16 s + 8 h + e
+  constexpr int NDMA = 4 + (BM == CODES ? 3 : 4);
+  static_assert(!GATED || (AM == ROWS && BM == ROWS), "gated: both operands by rows");
+  __shared__ Slot sl0, sl1, sl2, sl3;
+  Slot* const ring[NSLOT] = {&sl0, &sl1, &sl2, &sl3};
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  typedef __attribute__((address_space(3))) v4s* lds_v4s;
+
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3, dw = wave & 3;
+  const int tiles_n = (g.cols + (GATED ? TB / 2 : TB) - 1) / (GATED ? TB / 2 : TB), tiles_mp = (g.rows + TB - 1) / TB;
+  int tm, tn;
+  tile_of(blockIdx.x, gridDim.x, tiles_mp * g.probs, tiles_n, tm, tn);
+  const int prob = tm / tiles_mp, m0 = (tm % tiles_mp) * TB, n0 = tn * (GATED ? TB / 2 : TB);
+  const int all = g.steps * g.segs, s_lo = (int)((long long)all * blockIdx.y / g.splits),
+            s_hi = (int)((long long)all * (blockIdx.y + 1) / g.splits), S = s_hi - s_lo;
+
+  // ---- copies: instruction q of DMA wave dw, the lane's source offset (with OOB) and contraction index
+  int va[4], vb[4];
+  int ka, kb;   // ROWS: the chunk's contraction offset in a step
+  ka = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+  kb = ka;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (AM == ROWS) {
+      const int row = 64 * dw + 16 * q + (lane >> 2);
+      va[q] = (row * g.lda + ka) * 2 | (m0 + row < g.rows ? 0 : OOB);
+    } else {
+      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk, PERM);
+      va[q] = (kk * g.lda + 8 * c) * 2 | (m0 + 8 * c < g.rows ? 0 : OOB);
+    }
+    if constexpr (GATED) {
+      const int row = 32 * dw + 16 * (q & 1) + (lane >> 2);
+      vb[q] = (row * g.ldb + kb) * 2 | (n0 + row < g.cols ? 0 : OOB);
+    } else if constexpr (BM == ROWS) {
+      const int row = 64 * dw + 16 * q + (lane >> 2);
+      vb[q] = (row * g.ldb + kb) * 2 | (n0 + row < g.cols ? 0 : OOB);
+    } else if constexpr (BM == COLS) {
+      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk, PERM);
+      vb[q] = (kk * g.ldb + 8 * c) * 2 | (n0 + 8 * c < g.cols ? 0 : OOB);
+    } else {
+      const int row = 64 * dw + 32 * (q & 1) + (lane >> 1);
+      vb[q] = row * 32 + 16 * ((lane & 1) ^ ((row >> 3) & 1)) | (n0 + row < g.cols ? 0 : OOB);
+    }
+  }
+  const int vs = 64 * dw + 4 * (lane & 15);   // CODES: this DMA wave's 64 scales
+  auto clamp31 = [](long long v) { return (int)(v < 0x7FFFFFFFLL ? v : 0x7FFFFFFFLL); };
+  auto rows_rsrc = [&](const void* p, int ld, int r0, int rows, int k0) {   // rows r0.., contraction from k0
+    const uint16_t* q = static_cast<const uint16_t*>(p) + (size_t)r0 * ld + k0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(q), 0, clamp31(((long long)(rows - r0 - 1) * ld + g.K - k0) * 2), RSRC_W3);
+  };
+  auto cols_rsrc = [&](const void* p, int ld, int c0, int cols, int k0) {   // contraction rows k0.., columns c0..
+    const uint16_t* q = static_cast<const uint16_t*>(p) + (size_t)k0 * ld + c0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(q), 0, clamp31(((long long)(g.K - k0 - 1) * ld + cols - c0) * 2), RSRC_W3);
+  };
+  auto dma = [&](int i, Slot* sl) {   // step i of this block's; past the end: zeros
+    const int past = i < S ? 0 : OOB, s = s_lo + min(i, S - 1), seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
+    const void* pa = g.A[prob + seg];
+    if constexpr (AM == ROWS) {
+      const __amdgpu_buffer_rsrc_t r = rows_rsrc(pa, g.lda, m0, g.rows, k0);
+      const int o = past | (k0 + ka < g.K ? 0 : OOB);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * dw + q)), 16, va[q] | o, 0, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t r = cols_rsrc(pa, g.lda, m0, g.rows, k0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int o = past | (k0 + 2 * (4 * dw + q) + (lane >> 5) < g.K ? 0 : OOB);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * dw + q)), 16, va[q] | o, 0, 0, 0);
+      }
+    }
+    if constexpr (GATED) {
+      const __amdgpu_buffer_rsrc_t r0 = rows_rsrc(g.B[0], g.ldb, n0, g.cols, k0), r1 = rows_rsrc(g.B[1], g.ldb, n0, g.cols, k0);
+      const int o = past | (k0 + kb < g.K ? 0 : OOB);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
+    } else if constexpr (BM == ROWS) {
+      const __amdgpu_buffer_rsrc_t r = rows_rsrc(g.B[seg], g.ldb, n0, g.cols, k0);
+      const int o = past | (k0 + kb < g.K ? 0 : OOB);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
+    } else if constexpr (BM == COLS) {
+      const __amdgpu_buffer_rsrc_t r = cols_rsrc(g.B[seg], g.ldb, n0, g.cols, k0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int o = past | (k0 + 2 * (4 * dw + q) + (lane >> 5) < g.K ? 0 : OOB);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
+      }
+    } else {
+      const size_t c = (size_t)s * g.cols + n0;
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(static_cast<const uint8_t*>(g.B[0]) + c * 32), 0, clamp31((long long)(g.cols - n0) * 32), RSRC_W3);
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.scales + c), 0, g.cols - n0, RSRC_W3);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (2 * dw + q)), 16, vb[q] | past, 0, 0, 0);
+      if (lane < 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(sl->b + 8192 + 64 * dw), 4, vs | past, 0, 0, 0);
+    }
+  };
+
+  // ---- operands of sub-step s (16 of the contraction) of a slot
+  int ra[4], rb[4];   // LDS offsets: ROWS [s]; COLS [tile]
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int i16 = lane & 15, mh = (lane >> 4) & 1, kk = (PERM ? 16 : 8) * lh + (i16 >> 2), sw = cols_sw(kk, PERM);
+    if (AM == ROWS)
+      ra[i] = (128 * wm + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
+    else
+      ra[i] = kk * 512 + 16 * ((16 * wm + 4 * i + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
+    if (BM == ROWS)
+      rb[i] = (64 * wn + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
+    else if (BM == COLS)
+      rb[i] = kk * 512 + 16 * ((8 * wn + 4 * (i & 1) + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
+    else
+      rb[i] = sw_off32(64 * wn + lr, lh) + 1024 * (i & 1);
+  }
+  auto tr = [](const uint8_t* p) { return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)p)); };
+  auto two = [](v2i x, v2i y) { return v4i{x[0], x[1], y[0], y[1]}; };
+  auto rd = [&](Slot* sl, int s, v4i (&A)[4], v4i (&B)[2]) {
+    constexpr int SUB = (PERM ? 8 : 16) * 512;   // bytes from sub-step 0 to 1 in a COLS slot
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (AM == ROWS)
+        A[i] = *reinterpret_cast<const v4i*>(sl->a + ra[s] + 2048 * i);
+      else
+        A[i] = two(tr(sl->a + ra[i] + SUB * s), tr(sl->a + ra[i] + SUB * s + 4 * 512));
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (BM == ROWS) {
+        B[j] = *reinterpret_cast<const v4i*>(sl->b + rb[s] + 2048 * j);
+      } else if constexpr (BM == COLS) {
+        B[j] = two(tr(sl->b + rb[j] + SUB * s), tr(sl->b + rb[j] + SUB * s + 4 * 512));
+      } else {
+        const v2i c = *reinterpret_cast<const v2i*>(sl->b + rb[j] + 8 * s);
+        const uint32_t e = sl->b[8192 + 64 * wn + 32 * j + lr];
+        const float sc = e == 255u ? __uint_as_float(0x7FC00000u) : e == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int w = c[d >> 1] >> (16 * (d & 1));
+          B[j][d] = (int)pack_bf16x2((float)(int8_t)w * sc, (float)(int8_t)(w >> 8) * sc);
+        }
+      }
+    }
+  };
+
+  v16f acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  v4i A[2][4], B[2][2];
+  const bool dma_wave = wave < 4;
+  if (dma_wave) {
+#pragma unroll
+    for (int i = 0; i < NSLOT - 1; ++i) dma(i, ring[i]);
+    wait_vmcnt<NDMA * (NSLOT - 2)>();
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  rd(ring[0], 0, A[0], B[0]);
+  auto main_loop = [&](auto tag) {
+    constexpr bool D = decltype(tag)::value;
+    for (int i0 = 0; i0 < S; i0 += NSLOT) {
+#pragma unroll
+      for (int u = 0; u < NSLOT; ++u) {
+        if (D) wait_vmcnt<NDMA>();   // the next step has landed; the barrier frees the previous slot
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");   // the other waves' copies change the slots: no read moves over it
+        __builtin_amdgcn_sched_barrier(0);
+        rd(ring[u], 1, A[1], B[1]);
+        if (D) dma(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(A[0][i]), as_bf16x8(B[0][j]), acc[i][j], 0, 0, 0);
+        rd(ring[(u + 1) % NSLOT], 0, A[0], B[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(A[1][i]), as_bf16x8(B[1][j]), acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  if (dma_wave)
+    main_loop(std::true_type{});
+  else
+    main_loop(std::false_type{});
+  wait_vmcnt<0>();   // no LDS DMA may outlive the block
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  // ---- epilogue: lane holds column lr and rows 8 (v / 4) + 4 lh + v % 4 of each tile
+  uint8_t* stage = nullptr;
+#pragma unroll
+  for (int w = 0; w < 8; ++w)
+    if (wave == w) stage = (w & 1) ? ring[w >> 1]->b : ring[w >> 1]->a;   // 16 KB to a wave
+  const int r0 = m0 + 128 * wm;
+  if constexpr (EPI == OUT_BF16) {
+    store_block<0, 2>(acc, stage, static_cast<uint16_t*>(g.out[prob]), g.ldo, g.rows, g.cols, r0, n0 + 64 * wn, lane);
+  } else if constexpr (EPI == OUT_F32) {
+    float* out = static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int row = r0 + 32 * i + 8 * (v >> 2) + 4 * lh + (v & 3);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = n0 + 64 * wn + 32 * j + lr;
+          if (row < g.rows && col < g.cols) out[(size_t)row * g.ldo + col] = acc[i][j][v];
+        }
+      }
+  } else {
+    const int c0 = n0 + 32 * wn, col = c0 + lr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        float a, slope;
+        act_of(g.act, acc[i][0][v], a, slope);
+        if constexpr (EPI == OUT_GATED) {
+          acc[i][0][v] = a * acc[i][1][v];
+        } else {
+          const int row = r0 + 32 * i + 8 * (v >> 2) + 4 * lh + (v & 3);
+          const float dh = row < g.rows && col < g.cols ? bf16f(g.dH[(size_t)row * g.lddh + col]) : 0.f;
+          acc[i][0][v] = dh * acc[i][1][v] * slope;
+          acc[i][1][v] = dh * a;
+        }
+      }
+    store_block<0, 1>(acc, stage, static_cast<uint16_t*>(g.out[0]), g.ldo, g.rows, g.cols, r0, c0, lane);
+    if constexpr (EPI == OUT_GATED_GRAD)
+      store_block<1, 1>(acc, stage, static_cast<uint16_t*>(g.out[1]), g.ldo, g.rows, g.cols, r0, c0, lane);
+  }
+}
+
+// The planes of a split contraction added in order: out[i] = sum_s part[s][i], fp32 or rounded to bf16.
+template <class T>
+__global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restrict__ part, int splits, long long n, T* __restrict__ out) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;   // n is a multiple of 8
+  float4 s = *reinterpret_cast<const float4*>(part + i);
+  for (int q = 1; q < splits; ++q) {
+    const float4 v = *reinterpret_cast<const float4*>(part + q * n + i);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4*>(out + i) = s;
+  else
+    *reinterpret_cast<uint2*>(out + i) = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
+}
+
+// ------------------------------------------------------------------- gated forward, 1 to 16 rows
+// A block takes 16 columns of H, its eight waves an eighth of the contraction each (interleaved by 64, so
+// the block reads whole lines of each weight row); X's operand comes straight from memory, where its few
+// rows stay in the caches. The waves' sums meet in LDS in wave order. Lane (r = lane % 16, j = lane / 16)
+// takes the contraction 64 i + 16 j + 0..15 of weight row r and of X row r in two operands.
+constexpr int GT_WAVES = 8;
+__global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16_t* __restrict__ X, int M, int K, int ldx,
+                                                                    const uint16_t* __restrict__ Wg,
+                                                                    const uint16_t* __restrict__ Wu, int ldw, int F, int act,
+                                                                    uint16_t* __restrict__ H, int ldh) {
+  __shared__ __attribute__((aligned(16))) float red[GT_WAVES][2][16][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, j = lane >> 4;
+  const int f = min(blockIdx.x * 16 + r, F - 1);   // rows past the end repeat the last one
+  const uint16_t *wg = Wg + (size_t)f * ldw, *wu = Wu + (size_t)f * ldw, *x = X + (size_t)min(r, M - 1) * ldx;
+  const v4i zero = {0, 0, 0, 0};
+  v4f ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
+  for (int k0 = 64 * wave; k0 < K; k0 += 64 * GT_WAVES) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int k = k0 + 16 * j + 8 * s;
+      const bool in = k < K;   // K is a multiple of 8
+      const v4i a = in && r < M ? *reinterpret_cast<const v4i*>(x + k) : zero;
+      const v4i b = in ? *reinterpret_cast<const v4i*>(wg + k) : zero, c = in ? *reinterpret_cast<const v4i*>(wu + k) : zero;
+      ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), ag, 0, 0, 0);
+      au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(c), au, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    red[wave][0][4 * j + v][r] = ag[v];
+    red[wave][1][4 * j + v][r] = au[v];
+  }
+  __syncthreads();
+  const int m = threadIdx.x >> 4, c = threadIdx.x & 15, col = blockIdx.x * 16 + c;
+  if (m >= M || col >= F) return;   // threads 0..255 of 512 have a row below 16
+  float gs = 0.f, us = 0.f;
+#pragma unroll
+  for (int w = 0; w < GT_WAVES; ++w) {
+    gs += red[w][0][m][c];
+    us += red[w][1][m][c];
+  }
+  float a, slope;
+  act_of(act, gs, a, slope);
+  H[(size_t)m * ldh + col] = (uint16_t)pack_bf16x2(a * us, 0.f);
+}
+
+// ----------------------------------------------------------------------------- launch helpers
+inline int tiles_of(int n, int t) { return (n + t - 1) / t; }
+
+template <int AM, int BM, int EPI>
+hipError_t launch(const GemmArgs& g, hipStream_t st) {
+  constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
+  const long long blocks = (long long)tiles_of(g.rows, TB) * g.probs * tiles_of(g.cols, GATED ? TB / 2 : TB);
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI>), dim3((unsigned)blocks, g.splits), dim3(GM_THREADS), 0, st, g);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t join(const float* part, int splits, long long n, T* out, hipStream_t st) {
+  hipLaunchKernelGGL((gemm16_join_kernel<T>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, part, splits, n, out);
+  return hipGetLastError();
+}
+
+// Parts of the contraction: as many as give every compute unit a block, each at least 8 steps long.
+int splits_of(long long blocks, int steps) {
+  long long s = 256 / blocks;
+  if (s > steps / 8) s = steps / 8;
+  return s < 1 ? 1 : (int)s;
+}
+
+bool gated_shape_ok(int M, int K, int F) {
+  return M >= 1 && K >= 8 && F >= 8 && K % 8 == 0 && F % 8 == 0 && M <= (1 << 26) && K <= GM_MAX_LD && F <= GM_MAX_LD;
+}
+bool ld_ok(int ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= GM_MAX_LD; }
+
+// workspace of the backward pass: dG, dU [M][F] bf16, then the planes of dX's split contraction
+size_t gated_hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
+int gated_dx_splits(int M, int K, int F) {
+  return splits_of((long long)tiles_of(M, TB) * tiles_of(K, TB), 2 * tiles_of(F, KSTEP));
+}
+
+}  // namespace
+
+// ================================================================================ C ABI (device)
+extern "C" {
+
+size_t w4a4_gated_forward_bytes(int M, int K, int F) {
+  (void)M, (void)K, (void)F;
+  return 0;
+}
+
+w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg, const uint16_t* Wu, int ldw,
+                                 int F, int act, uint16_t* H, int ldh, void* ws, w4a4_stream_t stream) {
+  (void)ws;
+  if (act != W4A4_ACT_SILU && act != W4A4_ACT_GELU) return W4A4_ERR_UNSUPPORTED;
+  if (!gated_shape_ok(M, K, F) || !ld_ok(ldx, K) || !ld_ok(ldw, K) || !ld_ok(ldh, F)) return W4A4_ERR_INVALID_ARG;
+  if (!X || !Wg || !Wu || !H || !aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H)) return W4A4_ERR_INVALID_ARG;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (M <= 16) {
+    hipLaunchKernelGGL(gated_token_kernel, dim3(tiles_of(F, 16)), dim3(64 * GT_WAVES), 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
+    e = hipGetLastError();
+  } else {
+    GemmArgs g{};
+    g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = H;
+    g.lda = ldx, g.ldb = ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
+    g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP), g.act = act;
+    e = launch<ROWS, ROWS, OUT_GATED>(g, st);
+  }
+  return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+size_t w4a4_gated_backward_bytes(int M, int K, int F) {
+  if (!gated_shape_ok(M, K, F)) return 0;
+  const int sp = gated_dx_splits(M, K, F);
+  return 2 * gated_hidden_bytes(M, F) + (sp > 1 ? (size_t)sp * M * K * 4 : 0);
+}
+
+w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg,
+                                  const uint16_t* Wu, int ldw, int F, int act, uint16_t* dX, uint16_t* dWg, uint16_t* dWu,
+                                  void* ws, w4a4_stream_t stream) {
+  if (act != W4A4_ACT_SILU && act != W4A4_ACT_GELU) return W4A4_ERR_UNSUPPORTED;
+  if (!gated_shape_ok(M, K, F) || !ld_ok(lddh, F) || !ld_ok(ldx, K) || !ld_ok(ldw, K)) return W4A4_ERR_INVALID_ARG;
+  if (!dH || !X || !Wg || !Wu || !dX || !dWg || !dWu || !ws) return W4A4_ERR_INVALID_ARG;
+  if (!aligned16(dH) || !aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(dX) || !aligned16(dWg) ||
+      !aligned16(dWu) || !aligned16(ws))
+    return W4A4_ERR_INVALID_ARG;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  uint16_t* dG = static_cast<uint16_t*>(ws);
+  uint16_t* dU = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + gated_hidden_bytes(M, F));
+  float* planes = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * gated_hidden_bytes(M, F));
+
+  GemmArgs g{};   // both projections again, then dG and dU rounded to bf16, the operands of what follows
+  g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
+  g.lda = ldx, g.ldb = ldw, g.ldo = F, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
+  g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP), g.act = act;
+  if (launch<ROWS, ROWS, OUT_GATED_GRAD>(g, st) != hipSuccess) return W4A4_ERR_HIP;
+
+  GemmArgs x{};   // dX = [dG dU] [Wg; Wu]
+  x.A[0] = dG, x.A[1] = dU, x.B[0] = Wg, x.B[1] = Wu;
+  x.lda = F, x.ldb = ldw, x.ldo = K, x.rows = M, x.cols = K, x.K = F;
+  x.segs = 2, x.probs = 1, x.steps = tiles_of(F, KSTEP), x.splits = gated_dx_splits(M, K, F);
+  x.out[0] = x.splits > 1 ? static_cast<void*>(planes) : dX;
+  if ((x.splits > 1 ? launch<ROWS, COLS, OUT_F32>(x, st) : launch<ROWS, COLS, OUT_BF16>(x, st)) != hipSuccess) return W4A4_ERR_HIP;
+  if (x.splits > 1 && join(planes, x.splits, (long long)M * K, dX, st) != hipSuccess) return W4A4_ERR_HIP;
+
+  GemmArgs w{};   // dWg = dG^T X, dWu = dU^T X
+  w.A[0] = dG, w.A[1] = dU, w.B[0] = X, w.out[0] = dWg, w.out[1] = dWu;
+  w.lda = F, w.ldb = ldx, w.ldo = K, w.rows = F, w.cols = K, w.K = M;
+  w.segs = 1, w.probs = 2, w.splits = 1, w.steps = tiles_of(M, KSTEP);
+  return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+static int weight_grad_splits(int M, int N, int K) {
+  return splits_of((long long)tiles_of(N, TB) * tiles_of(K, TB), tiles_of(M, KSTEP));
+}
+static bool weight_grad_shape_ok(int M, int N, int K) {
+  return checkpoint_shape_ok(M, K) && N >= 8 && N % 8 == 0 && N <= GM_MAX_LD && K <= GM_MAX_LD;
+}
+
+size_t w4a4_checkpoint_weight_grad_bytes(int M, int N, int K) {
+  if (!weight_grad_shape_ok(M, N, K)) return 0;
+  return (size_t)weight_grad_splits(M, N, K) * N * K * 4;
+}
+
+w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const int8_t* codes, const uint8_t* scales, int M,
+                                          int N, int K, void* dW, int out_dtype, void* ws, w4a4_stream_t stream) {
+  if (out_dtype != W4A4_DTYPE_BF16 && out_dtype != W4A4_DTYPE_F32) return W4A4_ERR_UNSUPPORTED;
+  if (!weight_grad_shape_ok(M, N, K) || !ld_ok(lddy, N)) return W4A4_ERR_INVALID_ARG;
+  if (!dY || !codes || !scales || !dW || !ws || !aligned16(dY) || !aligned16(codes) || !aligned16(dW) || !aligned16(ws) ||
+      (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return W4A4_ERR_INVALID_ARG;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  GemmArgs g{};
+  g.A[0] = dY, g.B[0] = codes, g.scales = scales;
+  g.lda = lddy, g.ldo = K, g.rows = N, g.cols = K, g.K = M;
+  g.segs = g.probs = 1, g.steps = tiles_of(M, KSTEP), g.splits = weight_grad_splits(M, N, K);
+  hipError_t e;
+  if (g.splits == 1) {
+    g.out[0] = dW;
+    e = out_dtype == W4A4_DTYPE_F32 ? launch<COLS, CODES, OUT_F32>(g, st) : launch<COLS, CODES, OUT_BF16>(g, st);
+  } else {
+    float* planes = static_cast<float*>(ws);
+    g.out[0] = planes;
+    e = launch<COLS, CODES, OUT_F32>(g, st);
+    if (e == hipSuccess)
+      e = out_dtype == W4A4_DTYPE_F32 ? join(planes, g.splits, (long long)N * K, static_cast<float*>(dW), st)
+                                      : join(planes, g.splits, (long long)N * K, static_cast<uint16_t*>(dW), st);
+  }
+  return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+}  // extern "C"

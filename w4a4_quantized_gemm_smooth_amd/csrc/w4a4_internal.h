@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "w4a4.h"
+#include "w4a4_ops.h"
 
 namespace w4a4 {
 
@@ -82,6 +83,12 @@ inline size_t w8_xscale_floats(int M, int K) { return size_t(rows_pad_of(M)) * s
 // Largest activation row stride (elements) the activation kernel addresses: 16 rows of it must
 // stay below 2^31 bytes (32-bit buffer offsets).
 constexpr int QA_MAX_LDX = 1 << 26;
+
+// 8-bit checkpoints: channels in multiples of 8 (16-byte rows); blocks x channels fit a launch grid
+inline bool checkpoint_shape_ok(int M, int K) {
+  return M >= 1 && M <= (1 << 30) && K >= 8 && K % 8 == 0 && K <= (1 << 26) &&
+         ((long long)M + W4A4_CHECKPOINT_BLOCK - 1) / W4A4_CHECKPOINT_BLOCK * ((K + 1023) / 1024) <= INT_MAX;
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,0 +1,375 @@
+// The layer for 1 to 16 rows (single tokens of a few sequences): 4-bit weights times 16-bit
+// activations, with the low-rank branch,
+//     y[m][n] = sum_g s[n,g] sum_{k in g} q[n,k] x^[m][k] + sum_i t[m][i] L2[i][n] (+ bias[n]),
+//     x^ = fp32(x / lambda),  t = x^ L1,
+// bound by reading the codes once (K/2 bytes a row plus a scale per group). The activations are not
+// quantized: x^ goes to the matrix unit as two bf16 numbers hi + lo (16 significant bits), which is
+// free for up to 8 rows, since a 16-row operand then holds hi in rows 0..7 and lo in rows 8..15.
+//
+// INT4: the unit's operand for a code q is the bf16 number 16 + (q + 8), whose mantissa takes the four
+// bits of q + 8 as they are, so two codes cost a shift and an and-or; the accumulator starts at
+// -24 sum x^, which takes the offset out again (the sums of each group are made once, with x^).
+// MXFP4: the conversion instruction gives the E2M1 values in bf16. Either way a group's (block's) sum
+// is one fp32 accumulator that is scaled into the total by one FMA.
+//
+// Weights layout (w4a4_matvec_weights): per tile of 16 rows and pair of 64-groups 1 KB, 16 bytes to a
+// lane, in the order the lanes take them, so a wave's load is one contiguous KB; a dword d of lane
+// (r = lane % 16, j = lane / 16) holds the codes k = 64 (2p + d/2) + 32 (d % 2) + 8 j + 0..7 of row r.
+// After all codes: per tile, pair and row a dword of scales (two bf16, or four E8M0 bytes).
+//
+// Work split: a block of 8 waves takes 128 rows of W and a slice of K; x^ of the slice is made once a
+// block, in LDS; a wave takes 16 rows and issues all its loads of codes before that. A second kernel
+// adds the slices in slice order and the low-rank branch, whose down projection t runs in blocks of
+// its own beside the first kernel's others.
+#include "w4a4_device_common.h"
+
+using namespace w4a4;
+using namespace w4a4::dev;
+
+namespace {
+
+constexpr int MV_WAVES = 8, MV_THREADS = 64 * MV_WAVES, MV_ROWS = 16 * MV_WAVES;  // rows of W a block
+constexpr int MV_MAX_M = W4A4_MATVEC_MAX_ROWS;
+
+inline int mv_tiles(int N) { return (N + 15) / 16; }
+inline int mv_pairs(int K) { return (K + 2 * W4A4_GROUP - 1) / (2 * W4A4_GROUP); }
+inline int mv_blocks(int N) { return (N + MV_ROWS - 1) / MV_ROWS; }
+// pairs of groups a slice: the longest slice that still gives two blocks to each compute unit
+inline int mv_slice(int N, int K) {
+  for (int sp = 8; sp > 1; sp /= 2)
+    if (mv_blocks(N) * ((mv_pairs(K) + sp - 1) / sp) >= 512) return sp;
+  return 1;
+}
+
+__device__ __forceinline__ float e8m0(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7FC00000u) : b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
+
+// ------------------------------------------------------------------------------ weights layout
+__global__ __launch_bounds__(256) void matvec_weights_kernel(const uint8_t* __restrict__ codes, const void* __restrict__ scales,
+                                                             int N, int K, bool mx, uint8_t* __restrict__ wv) {
+  const int G = K / W4A4_GROUP, P = (G + 1) / 2, tiles = (N + 15) / 16;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long long)tiles * P * 64) return;
+  const int lane = (int)(i & 63), p = (int)((i >> 6) % P), tile = (int)((i >> 6) / P), r = lane & 15, j = lane >> 4;
+  const int n = tile * 16 + r;
+  uint32_t w[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int g = 2 * p + (d >> 1), k = g * W4A4_GROUP + 32 * (d & 1) + 8 * j;
+    uint32_t c = 0u;
+    if (n < N && g < G) c = *reinterpret_cast<const uint32_t*>(codes + (size_t)n * (K / 2) + k / 2);
+    if (!mx) {   // q + 8, element 2i in nibble i and 2i + 1 in nibble 4 + i
+      c ^= 0x88888888u;
+      uint32_t o = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o |= ((c >> (4 * e)) & 15u) << (4 * ((e >> 1) + 4 * (e & 1)));
+      c = o;
+    }
+    w[d] = c;
+  }
+  reinterpret_cast<uint4*>(wv)[i] = uint4{w[0], w[1], w[2], w[3]};
+  if (j == 0) {
+    uint32_t s = 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int g = 2 * p + h;
+      if (n >= N || g >= G) continue;
+      if (mx) {
+        const uint8_t* b = static_cast<const uint8_t*>(scales) + (size_t)n * (K / W4A4_MX_BLOCK) + 2 * g;
+        s |= ((uint32_t)b[0] | (uint32_t)b[1] << 8) << (16 * h);
+      } else {
+        s |= (uint32_t)static_cast<const uint16_t*>(scales)[(size_t)n * G + g] << (16 * h);
+      }
+    }
+    reinterpret_cast<uint32_t*>(wv + (size_t)tiles * P * 1024)[((size_t)tile * P + p) * 16 + r] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------------- main kernel
+// x^ of the block's slice -> LDS: rows 0..M-1 hi, M..2M-1 lo, row 2M zeros, of `stride` bytes (a
+// multiple of 64 not of 128: 16-byte reads of 16 rows x 4 chunks then meet each bank equally often);
+// and -24 times the group sums, [2 SP][16], by the row of the matrix operand. K and beyond: zeros.
+template <int SP>
+__device__ __forceinline__ void stage_x(const uint16_t* __restrict__ X, int ldx, const float* __restrict__ inv, int M, int K,
+                                        int kbase, uint8_t* xs, float* sums, bool two) {
+  constexpr int STRIDE = SP * 256 + 64, CH = SP * 16;
+  for (int i = threadIdx.x; i < 2 * SP * 16; i += MV_THREADS) sums[i] = 0.f;
+  for (int i = threadIdx.x; i < CH; i += MV_THREADS) *reinterpret_cast<uint4*>(xs + 2 * M * STRIDE + 16 * i) = uint4{0u, 0u, 0u, 0u};
+  __syncthreads();
+  for (int i = threadIdx.x; i < M * CH; i += MV_THREADS) {
+    const int m = i / CH, c = i % CH, k = kbase + 8 * c;
+    uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+    float sh = 0.f, sl = 0.f;
+    if (k < K) {   // K is a multiple of 64
+      const uint4 v = *reinterpret_cast<const uint4*>(X + (size_t)m * ldx + k);
+      const float4 a = *reinterpret_cast<const float4*>(inv + k), b = *reinterpret_cast<const float4*>(inv + k + 4);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const float il[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const float x0 = __uint_as_float(w[d] << 16) * il[2 * d], x1 = __uint_as_float(w[d] & 0xFFFF0000u) * il[2 * d + 1];
+        hi[d] = pack_bf16x2(x0, x1);
+        const float h0 = __uint_as_float(hi[d] << 16), h1 = __uint_as_float(hi[d] & 0xFFFF0000u);
+        lo[d] = pack_bf16x2(x0 - h0, x1 - h1);
+        sh += h0 + h1;
+        sl += __uint_as_float(lo[d] << 16) + __uint_as_float(lo[d] & 0xFFFF0000u);
+      }
+    }
+    *reinterpret_cast<uint4*>(xs + m * STRIDE + 16 * c) = uint4{hi[0], hi[1], hi[2], hi[3]};
+    *reinterpret_cast<uint4*>(xs + (M + m) * STRIDE + 16 * c) = uint4{lo[0], lo[1], lo[2], lo[3]};
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {   // the 8 threads of a group (whole or absent: CH is a multiple of 8)
+      sh += __shfl_xor(sh, o);
+      sl += __shfl_xor(sl, o);
+    }
+    if ((c & 7) == 0) {
+      sums[(c >> 3) * 16 + m] = -24.f * (two ? sh + sl : sh);
+      if (!two) sums[(c >> 3) * 16 + 8 + m] = -24.f * sl;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+// TWO: M > 8, the hi and lo rows are two operands. Blocks: index = slice * (nb + tb) + b; b < nb the
+// rows of W, b = nb (where rank > 0) the down projection.
+template <bool MX, bool TWO, int SP>
+__global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __restrict__ X, int ldx,
+                                                            const float* __restrict__ inv, const uint16_t* __restrict__ l1t,
+                                                            const uint8_t* __restrict__ wv, int M, int N, int K, int rp,
+                                                            int nb, float* __restrict__ part, float* __restrict__ tpart) {
+  constexpr int STRIDE = SP * 256 + 64;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* sums = reinterpret_cast<float*>(lds);
+  uint8_t* xs = lds + 2 * SP * 16 * 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
+  const int per = nb + (rp > 0 ? 1 : 0), slice = blockIdx.x / per, b = blockIdx.x % per;
+  const int G = K / W4A4_GROUP, P = (G + 1) / 2, tiles = (N + 15) / 16, p0 = slice * SP, np = min(SP, P - p0);
+  const int row_hi = TWO ? (r < M ? r : 2 * M) : (r < 8 ? (r < M ? r : 2 * M) : (r - 8 < M ? M + r - 8 : 2 * M));
+  const uint8_t* xh = xs + row_hi * STRIDE + 16 * j;
+  const uint8_t* xl = xs + (r < M ? M + r : 2 * M) * STRIDE + 16 * j;   // TWO only
+
+  if (b == nb) {   // t: 16 rows of L1^T a wave; waves beyond the rank's tiles take other pairs
+    const int rt = rp / 16, nsub = MV_WAVES / rt, tile = wave % rt, sub = wave / rt;
+    stage_x<SP>(X, ldx, inv, M, K, p0 * 128, xs, sums, TWO);
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    if (sub < nsub) {
+      for (int i = sub; i < np; i += nsub)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int k = (p0 + i) * 128 + 32 * d + 8 * j;
+          const v4i w = k < K ? *reinterpret_cast<const v4i*>(l1t + (size_t)(tile * 16 + r) * K + k) : v4i{0, 0, 0, 0};
+          acc = mfma16(*reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d), w, acc);
+          if (TWO) acc = mfma16(*reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d), w, acc);
+        }
+    }
+    if (!TWO) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] += __shfl_xor(acc[v], 32);
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(xs);   // [waves][16][16]: 8 KB; x^ is done with
+    if (TWO || j < 2) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * j + v) * 16 + r] = acc[v];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < M * rp; i += MV_THREADS) {
+      const int m = i / rp, c = i % rp;
+      float s = 0.f;
+      for (int q = 0; q < nsub; ++q) s += red[((q * rt + c / 16) * 16 + m) * 16 + (c & 15)];
+      tpart[(size_t)slice * M * rp + i] = s;
+    }
+    return;
+  }
+
+  const int tile = b * MV_WAVES + wave;
+  const bool live = tile < tiles;
+  const v4i* cw = reinterpret_cast<const v4i*>(wv) + ((size_t)(live ? tile : 0) * P + p0) * 64 + lane;
+  const uint32_t* sw = reinterpret_cast<const uint32_t*>(wv + (size_t)tiles * P * 1024) + ((size_t)(live ? tile : 0) * P + p0) * 16 + r;
+  v4i w[SP];
+  uint32_t sc[SP];
+#pragma unroll
+  for (int i = 0; i < SP; ++i) {
+    const int q = min(i, np - 1);
+    w[i] = cw[q * 64];
+    sc[i] = sw[q * 16];
+  }
+  stage_x<SP>(X, ldx, inv, M, K, p0 * 128, xs, sums, TWO);
+  if (!live) return;
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < SP; ++i) {
+    if (i >= np) break;
+    v4f pt = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t c = (uint32_t)w[i][d];
+      v4i op;
+      if constexpr (MX) {
+        op[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
+        op[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1));
+        op[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2));
+        op[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3));
+        pt = v4f{0.f, 0.f, 0.f, 0.f};
+      } else {
+        op[0] = (int)(((c << 3) & 0x00780078u) | 0x41804180u);
+        op[1] = (int)(((c >> 1) & 0x00780078u) | 0x41804180u);
+        op[2] = (int)(((c >> 5) & 0x00780078u) | 0x41804180u);
+        op[3] = (int)(((c >> 9) & 0x00780078u) | 0x41804180u);
+        if ((d & 1) == 0) pt = *reinterpret_cast<const v4f*>(sums + (2 * i + (d >> 1)) * 16 + 4 * j);
+      }
+      pt = mfma16(*reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d), op, pt);
+      if (TWO) pt = mfma16(*reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d), op, pt);
+      if (MX || (d & 1)) {
+        const float s = MX ? e8m0((sc[i] >> (8 * d)) & 255u) : (d == 1 ? __uint_as_float(sc[i] << 16) : __uint_as_float(sc[i] & 0xFFFF0000u));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] = fmaf(s, pt[v], acc[v]);
+      }
+    }
+  }
+  if (!TWO) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += __shfl_xor(acc[v], 32);
+  }
+  float* out = part + (size_t)slice * M * (tiles * 16) + tile * 16 + r;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int m = 4 * j + v;
+    if (m < M && (TWO || j < 2)) out[(size_t)m * (tiles * 16)] = acc[v];
+  }
+}
+
+// y = the slices' sums + t L2 + bias; a block 64 columns, a wave every fourth row.
+__global__ __launch_bounds__(256) void matvec_finish_kernel(const float* __restrict__ part, const float* __restrict__ tpart,
+                                                            int slices, const uint16_t* __restrict__ l2t,
+                                                            const uint16_t* __restrict__ bias, int M, int N, int rp,
+                                                            uint16_t* __restrict__ Y, int ldy) {
+  __shared__ float t[MV_MAX_M * W4A4_MAX_RANK];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * 64 + lane, np = (N + 15) / 16 * 16;
+  for (int i = threadIdx.x; i < M * rp; i += 256) {
+    float s = 0.f;
+    for (int q = 0; q < slices; ++q) s += tpart[(size_t)q * M * rp + i];
+    t[i] = s;
+  }
+  __syncthreads();
+  if (n >= N) return;
+  float acc[MV_MAX_M / 4];
+#pragma unroll
+  for (int i = 0; i < MV_MAX_M / 4; ++i) {
+    const int m = w + 4 * i;
+    acc[i] = 0.f;
+    if (m < M)
+      for (int q = 0; q < slices; ++q) acc[i] += part[((size_t)q * M + m) * np + n];
+  }
+  for (int c = 0; c < rp; c += 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(l2t + (size_t)n * rp + c);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < MV_MAX_M / 4; ++i) {
+      const int m = w + 4 * i;
+      if (m >= M) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        acc[i] = fmaf(t[m * rp + c + e], __uint_as_float((e & 1) ? (u[e >> 1] & 0xFFFF0000u) : (u[e >> 1] << 16)), acc[i]);
+    }
+  }
+  const float bb = bias ? bf16f(bias[n]) : 0.f;
+#pragma unroll
+  for (int i = 0; i < MV_MAX_M / 4; ++i) {
+    const int m = w + 4 * i;
+    if (m < M) Y[(size_t)m * ldy + n] = (uint16_t)pack_bf16x2(acc[i] + bb, 0.f);
+  }
+}
+
+template <bool MX, bool TWO, int SP>
+hipError_t launch(const uint16_t* X, int ldx, const float* inv, const uint16_t* l1t, const uint8_t* wv, int M, int N, int K,
+                  int rp, float* part, float* tpart, hipStream_t st) {
+  const int slices = (mv_pairs(K) + SP - 1) / SP, nb = mv_blocks(N);
+  size_t lds = (size_t)2 * SP * 16 * 4 + (size_t)(2 * M + 1) * (SP * 256 + 64);
+  if (lds < 2 * SP * 16 * 4 + 8192) lds = 2 * SP * 16 * 4 + 8192;   // the down projection's sums
+  if (lds > 65536) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<MX, TWO, SP>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (attr != hipSuccess) return attr;
+  }
+  hipLaunchKernelGGL((matvec_kernel<MX, TWO, SP>), dim3(slices * (nb + (rp > 0 ? 1 : 0))), dim3(MV_THREADS), lds, st, X, ldx, inv,
+                     l1t, wv, M, N, K, rp, nb, part, tpart);
+  return hipGetLastError();
+}
+
+template <bool MX, bool TWO>
+hipError_t dispatch(int sp, const uint16_t* X, int ldx, const float* inv, const uint16_t* l1t, const uint8_t* wv, int M, int N,
+                    int K, int rp, float* part, float* tpart, hipStream_t st) {
+  switch (sp) {
+    case 8: return launch<MX, TWO, 8>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
+    case 4: return launch<MX, TWO, 4>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
+    case 2: return launch<MX, TWO, 2>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
+    default: return launch<MX, TWO, 1>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
+  }
+}
+
+w4a4_status_t check_matvec(int M, int N, int K, int rank, int fmt) {
+  if (fmt != W4A4_FMT_INT4_G64 && fmt != W4A4_FMT_MXFP4_B32) return W4A4_ERR_UNSUPPORTED;
+  if (M > MV_MAX_M) return W4A4_ERR_INVALID_ARG;
+  return check_shape(M, N, K, rank, fmt);
+}
+
+}  // namespace
+
+// ================================================================================ C ABI (device)
+extern "C" {
+
+w4a4_status_t w4a4_matvec_sizes(int M, int N, int K, int rank, int fmt, size_t* wv, size_t* ws) {
+  const w4a4_status_t s = check_matvec(M, N, K, rank, fmt);
+  if (s != W4A4_OK) return s;
+  if (!wv || !ws) return W4A4_ERR_INVALID_ARG;
+  const size_t P = mv_pairs(K), tiles = mv_tiles(N), sp = mv_slice(N, K), slices = (P + sp - 1) / sp;
+  *wv = tiles * P * (1024 + 64);
+  *ws = slices * M * (tiles * 16 + rank_pad_of(rank)) * sizeof(float);
+  return W4A4_OK;
+}
+
+w4a4_status_t w4a4_matvec_weights(const uint8_t* codes, const void* scales, int N, int K, int fmt, uint8_t* wv,
+                                  w4a4_stream_t stream) {
+  const w4a4_status_t s = check_matvec(1, N, K, 0, fmt);
+  if (s != W4A4_OK) return s;
+  if (!codes || !scales || !wv || !aligned16(codes) || !aligned16(scales) || !aligned16(wv)) return W4A4_ERR_INVALID_ARG;
+  const size_t items = (size_t)mv_tiles(N) * mv_pairs(K) * 64;
+  hipLaunchKernelGGL(matvec_weights_kernel, dim3((unsigned)((items + 255) / 256)), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(stream), codes, scales, N, K, fmt == W4A4_FMT_MXFP4_B32, wv);
+  return hipGetLastError() == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+w4a4_status_t w4a4_matvec(const uint16_t* X, int M, int K, int ldx, const float* inv_lambda, const uint16_t* l1t,
+                          const uint8_t* wv, const uint16_t* l2t, const uint16_t* bias, uint16_t* Y, int ldy, int N,
+                          int rank, int fmt, void* ws, w4a4_stream_t stream) {
+  const w4a4_status_t s = check_matvec(M, N, K, rank, fmt);
+  if (s != W4A4_OK) return s;
+  if (ldx < K || ldx % 8 != 0 || ldx > QA_MAX_LDX || ldy < N) return W4A4_ERR_INVALID_ARG;
+  if (!X || !inv_lambda || !wv || !Y || !ws || (rank > 0 && (!l1t || !l2t))) return W4A4_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(inv_lambda) || !aligned16(wv) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(Y) & 1u) ||
+      (rank > 0 && (!aligned16(l1t) || !aligned16(l2t))) || (reinterpret_cast<uintptr_t>(bias) & 1u))
+    return W4A4_ERR_INVALID_ARG;
+  const int rp = rank_pad_of(rank), sp = mv_slice(N, K), slices = (mv_pairs(K) + sp - 1) / sp;
+  float* part = static_cast<float*>(ws);
+  float* tpart = part + (size_t)slices * M * (mv_tiles(N) * 16);
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool mx = fmt == W4A4_FMT_MXFP4_B32;
+  hipError_t e;
+  if (M <= 8)
+    e = mx ? dispatch<true, false>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st)
+           : dispatch<false, false>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st);
+  else
+    e = mx ? dispatch<true, true>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st)
+           : dispatch<false, true>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st);
+  if (e != hipSuccess) return W4A4_ERR_HIP;
+  hipLaunchKernelGGL(matvec_finish_kernel, dim3((N + 63) / 64), dim3(256), 0, st, part, tpart, slices, l2t, bias, M, N, rp, Y, ldy);
+  return hipGetLastError() == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+}  // extern "C"

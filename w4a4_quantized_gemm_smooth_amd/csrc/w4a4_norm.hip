@@ -1,0 +1,516 @@
+// Layer normalisation over rows and its gradients (training; the norm in front of a layer's
+// projections). For a row x of K elements:
+//     mu = sum(x) / K,  rstd = 1 / sqrt(sum((x - mu)^2) / K + eps),  h = (x - mu) rstd,
+//     y = h gamma + beta;
+//     d = dy gamma,  dx = rstd (d - mean(d) - h mean(d h)),  dgamma = sum_rows dy h,  dbeta = sum_rows dy.
+// Both directions read each element once: a row stays in the registers of the one or more waves that
+// own it (16-byte pieces, thread t of the row's T threads holding pieces t, t + T, ...), the
+// statistics are two sums over those registers (the squares around the mean, so a large common
+// offset costs no digits), everything in fp32. Bounded by memory.
+//
+// The backward kernel is persistent: a row group keeps its columns' dgamma and dbeta sums in
+// registers over all its rows, a block adds its row groups' sums in group order through LDS and
+// writes one partial row, and a second kernel adds the blocks' partial rows in block order, so the
+// result does not depend on timing.
+#include <type_traits>
+
+#include "w4a4_device_common.h"
+
+using namespace w4a4;
+using namespace w4a4::dev;
+
+namespace {
+
+// 16 bytes of a row at any element alignment (rows of an odd stride); global loads and stores of
+// gfx950 need none beyond the byte.
+template <class T> constexpr int VEC = 16 / sizeof(T);
+struct __attribute__((packed, aligned(2))) Piece2 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(4))) Piece4 { uint32_t w[4]; };
+template <class T> using Piece = std::conditional_t<sizeof(T) == 2, Piece2, Piece4>;
+
+__device__ __forceinline__ float to_f(uint16_t v) { return bf16f(v); }
+__device__ __forceinline__ float to_f(float v) { return v; }
+// one rounding, to nearest even (NaN and infinities kept)
+template <class T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ uint16_t from_f<uint16_t>(float v) { return (uint16_t)pack_bf16x2(v, 0.f); }
+
+// element e of a piece
+template <class T>
+__device__ __forceinline__ float get(const Piece<T>& p, int e) {
+  if constexpr (sizeof(T) == 2)
+    return __uint_as_float((e & 1) ? (p.w[e >> 1] & 0xFFFF0000u) : (p.w[e >> 1] << 16));
+  else
+    return __uint_as_float(p.w[e]);
+}
+
+// the piece of `row` that starts at element k0; elements at K and beyond read as 0
+template <class T>
+__device__ __forceinline__ Piece<T> load_piece(const T* row, int k0, int K) {
+  Piece<T> p = {{0u, 0u, 0u, 0u}};
+  if (k0 + VEC<T> <= K) {
+    p = *reinterpret_cast<const Piece<T>*>(row + k0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC<T>; ++e)
+      if (k0 + e < K) {
+        if constexpr (sizeof(T) == 2)
+          p.w[e >> 1] |= (uint32_t)row[k0 + e] << (16 * (e & 1));
+        else
+          p.w[e] = __float_as_uint(row[k0 + e]);
+      }
+  }
+  return p;
+}
+
+template <class T>
+__device__ __forceinline__ void store_piece(T* row, int k0, int K, const float (&v)[VEC<T>]) {
+  if (k0 + VEC<T> <= K) {
+    Piece<T> p;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p.w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p.w[e] = __float_as_uint(v[e]);
+    }
+    *reinterpret_cast<Piece<T>*>(row + k0) = p;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC<T>; ++e)
+      if (k0 + e < K) row[k0 + e] = from_f<T>(v[e]);
+  }
+}
+
+// the parameters of VEC<T> columns from k0 on (`none` where there are no parameters or no column)
+template <class T, class P>
+__device__ __forceinline__ void load_params(const P* p, int k0, int K, float none, float (&out)[VEC<T>]) {
+#pragma unroll
+  for (int e = 0; e < VEC<T>; ++e) out[e] = none;
+  if (!p) return;
+  if (k0 + VEC<T> <= K) {
+    constexpr int N = VEC<T> / VEC<P> > 0 ? VEC<T> / VEC<P> : 1;
+    if constexpr (VEC<T> >= VEC<P>) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const Piece<P> q = *reinterpret_cast<const Piece<P>*>(p + k0 + i * VEC<P>);
+#pragma unroll
+        for (int e = 0; e < VEC<P>; ++e) out[i * VEC<P> + e] = get<P>(q, e);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC<T>; ++e) out[e] = to_f(p[k0 + e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC<T>; ++e)
+      if (k0 + e < K) out[e] = to_f(p[k0 + e]);
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sums over the WPR waves that share a row, the same value in each of them. `red`: this call's own
+// [groups][WPR][N] floats of LDS.
+template <int WPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int group, int wave_in_row, int lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (WPR > 1) {
+    float* r = red + group * WPR * N;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[wave_in_row * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) s += r[w * N + i];
+      v[i] = s;
+    }
+  }
+}
+
+// WPR waves to a row, C pieces to a thread (K <= 64 WPR VEC C), blocks of WAVES waves. C = 0: rows of
+// any length, read again for each sum (they stay in the caches).
+template <class T, class P, int WPR, int C, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void norm_forward_kernel(const T* __restrict__ X, int M, int K, int ldx,
+                                                                  const P* __restrict__ gamma, const P* __restrict__ beta,
+                                                                  float eps, T* __restrict__ Y, int ldy,
+                                                                  float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int G = WAVES / WPR, V = VEC<T>, STEP = 64 * WPR * V;
+  __shared__ float red[2][G * WPR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = wave / WPR, wr = wave % WPR;
+  const long long row = (long long)blockIdx.x * G + group;
+  const bool in = row < M;   // rows past the end take part in the barriers on row M - 1's data
+  const T* x = X + (in ? row : M - 1) * (long long)ldx;
+  T* y = Y + (in ? row : M - 1) * (long long)ldy;
+  const int k0 = (wr * 64 + lane) * V;
+  Piece<T> v[C > 0 ? C : 1];
+  float s[1] = {0.f}, q[1] = {0.f};
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = load_piece<T>(x, k0 + c * STEP, K);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] += get<T>(v[c], e);
+  } else {
+    for (int k = k0; k < K; k += STEP) {
+      const Piece<T> p = load_piece<T>(x, k, K);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] += get<T>(p, e);
+    }
+  }
+  row_sum<WPR, 1>(s, red[0], group, wr, lane);
+  const float mu = s[0] / (float)K;
+  auto squares = [&](const Piece<T>& p, int k) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float d = get<T>(p, e) - mu;
+      q[0] += k + e < K ? d * d : 0.f;
+    }
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) squares(v[c], k0 + c * STEP);
+  } else {
+    for (int k = k0; k < K; k += STEP) squares(load_piece<T>(x, k, K), k);
+  }
+  row_sum<WPR, 1>(q, red[1], group, wr, lane);
+  const float rs = 1.0f / sqrtf(q[0] / (float)K + eps);
+  if (!in) return;
+  if (wr == 0 && lane == 0) {
+    mean[row] = mu;
+    rstd[row] = rs;
+  }
+  auto write = [&](const Piece<T>& p, int k) {
+    if (k >= K) return;
+    float g[V], b[V], o[V];
+    load_params<T, P>(gamma, k, K, 1.f, g);
+    load_params<T, P>(beta, k, K, 0.f, b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = (get<T>(p, e) - mu) * rs * g[e] + b[e];
+    store_piece<T>(y, k, K, o);
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) write(v[c], k0 + c * STEP);
+  } else {
+    for (int k = k0; k < K; k += STEP) write(load_piece<T>(x, k, K), k);
+  }
+}
+
+// GRADS: also the parameters' gradients, into part [gridDim.x][2][K]. C = 0 (rows of any length): no
+// register holds a row; the parameters' gradients come from norm_columns_kernel.
+template <class T, class P, int WPR, int C, int WAVES, bool GRADS>
+__global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
+    const T* __restrict__ dY, int lddy, const T* __restrict__ X, int ldx, const P* __restrict__ gamma,
+    const float* __restrict__ mean, const float* __restrict__ rstd, int M, int K, T* __restrict__ dX, int lddx,
+    float* __restrict__ part) {
+  constexpr int G = WAVES / WPR, V = VEC<T>, STEP = 64 * WPR * V, CC = C > 0 ? C : 1;
+  __shared__ float red[2][G * WPR * 2];
+  extern __shared__ float cols[];   // [2][K], GRADS only
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = wave / WPR, wr = wave % WPR;
+  const int k0 = (wr * 64 + lane) * V;
+  float dg[GRADS ? CC : 1][V] = {}, db[GRADS ? CC : 1][V] = {};
+  const long long stride = (long long)gridDim.x * G;
+  const long long first = (long long)blockIdx.x * G;   // every group makes the same number of turns
+  int turn = 0;
+  Piece<T> xv[CC], dv[CC];
+  auto fetch = [&](long long base) {
+    const long long row = base + group < M ? base + group : M - 1;
+#pragma unroll
+    for (int c = 0; c < CC; ++c) {
+      xv[c] = load_piece<T>(X + row * ldx, k0 + c * STEP, K);
+      dv[c] = load_piece<T>(dY + row * lddy, k0 + c * STEP, K);
+    }
+  };
+  if constexpr (C > 0) fetch(first);
+  for (long long base = first; base < M; base += stride, turn ^= 1) {
+    const bool in = base + group < M;
+    const long long row = in ? base + group : M - 1;
+    const float mu = mean[row], rs = rstd[row];
+    Piece<T> xc[CC], dc[CC];
+    if constexpr (C > 0) {   // this row's data in hand, the next row's on its way
+#pragma unroll
+      for (int c = 0; c < CC; ++c) {
+        xc[c] = xv[c];
+        dc[c] = dv[c];
+      }
+      if (base + stride < M) fetch(base + stride);
+    }
+    float s[2] = {0.f, 0.f};
+    auto sums = [&](const Piece<T>& x, const Piece<T>& d, int k, int c) {
+      float g[V];
+      load_params<T, P>(gamma, k, K, 1.f, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float h = (get<T>(x, e) - mu) * rs, dy = get<T>(d, e), t = dy * g[e];   // dy is 0 past K
+        s[0] += t;
+        s[1] += k + e < K ? t * h : 0.f;
+        if (GRADS && in) {
+          dg[c][e] += dy * h;
+          db[c][e] += dy;
+        }
+      }
+    };
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < CC; ++c) sums(xc[c], dc[c], k0 + c * STEP, c);
+    } else {
+      for (int k = k0; k < K; k += STEP)
+        sums(load_piece<T>(X + row * ldx, k, K), load_piece<T>(dY + row * lddy, k, K), k, 0);
+    }
+    row_sum<WPR, 2>(s, red[turn], group, wr, lane);
+    const float m1 = s[0] / (float)K, m2 = s[1] / (float)K;
+    auto write = [&](const Piece<T>& x, const Piece<T>& d, int k) {
+      if (k >= K || !in) return;
+      float g[V], o[V];
+      load_params<T, P>(gamma, k, K, 1.f, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float h = (get<T>(x, e) - mu) * rs;
+        o[e] = rs * (get<T>(d, e) * g[e] - m1 - h * m2);
+      }
+      store_piece<T>(dX + row * lddx, k, K, o);
+    };
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < CC; ++c) write(xc[c], dc[c], k0 + c * STEP);
+    } else {
+      for (int k = k0; k < K; k += STEP)
+        write(load_piece<T>(X + row * ldx, k, K), load_piece<T>(dY + row * lddy, k, K), k);
+    }
+  }
+  if constexpr (GRADS) {   // the block's sums, its row groups in order
+    for (int g = 0; g < G; ++g) {
+      if (group == g) {
+#pragma unroll
+        for (int c = 0; c < CC; ++c)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const int k = k0 + c * STEP + e;
+            if (k < K) {
+              cols[k] = g == 0 ? dg[c][e] : cols[k] + dg[c][e];
+              cols[K + k] = g == 0 ? db[c][e] : cols[K + k] + db[c][e];
+            }
+          }
+      }
+      __syncthreads();
+    }
+    float* out = part + (size_t)blockIdx.x * 2 * K;
+    for (int k = threadIdx.x; k < 2 * K; k += 64 * WAVES) out[k] = cols[k];
+  }
+}
+
+// The parameters' gradients of rows too long for registers: a block takes 64 columns and every
+// gridDim.y-th row, into part [gridDim.y][2][K].
+template <class T>
+__global__ __launch_bounds__(256) void norm_columns_kernel(const T* __restrict__ dY, int lddy, const T* __restrict__ X,
+                                                           int ldx, const float* __restrict__ mean,
+                                                           const float* __restrict__ rstd, int M, int K,
+                                                           float* __restrict__ part) {
+  __shared__ float red[4][64][2];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
+  float g = 0.f, b = 0.f;
+  if (k < K)
+    for (long long m = blockIdx.y * 4 + w; m < M; m += gridDim.y * 4) {
+      const float dy = to_f(dY[m * lddy + k]);
+      g += dy * ((to_f(X[m * ldx + k]) - mean[m]) * rstd[m]);
+      b += dy;
+    }
+  red[w][lane][0] = g;
+  red[w][lane][1] = b;
+  __syncthreads();
+  if (w == 0 && k < K) {
+    for (int i = 1; i < 4; ++i) {
+      g += red[i][lane][0];
+      b += red[i][lane][1];
+    }
+    part[(size_t)blockIdx.y * 2 * K + k] = g;
+    part[(size_t)blockIdx.y * 2 * K + K + k] = b;
+  }
+}
+
+// dgamma, dbeta: the rows of part [rows][2][K] added in a fixed order; 16 lanes of a block's 1024
+// threads' columns each take every 16th row.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part, int rows, int K,
+                                                           float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float red[16][65];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (k < 2 * K)
+    for (int r = w; r < rows; r += 16) s += part[(size_t)r * 2 * K + k];
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && k < 2 * K) {
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    if (k < K) {
+      if (dgamma) dgamma[k] = s;
+    } else if (dbeta) {
+      dbeta[k - K] = s;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- launch helpers
+constexpr int NORM_BLOCKS = 256;      // backward: persistent blocks, one a compute unit
+constexpr int NORM_MAX_K = 16384;     // longest row kept in registers
+
+template <class T, class P, int WPR, int C, int WAVES>
+hipError_t forward(const void* X, int M, int K, int ldx, const void* gamma, const void* beta, float eps, void* Y, int ldy,
+                   float* mean, float* rstd, hipStream_t st) {
+  constexpr int G = WAVES / WPR;
+  hipLaunchKernelGGL((norm_forward_kernel<T, P, WPR, C, WAVES>), dim3((M + G - 1) / G), dim3(64 * WAVES), 0, st,
+                     static_cast<const T*>(X), M, K, ldx, static_cast<const P*>(gamma), static_cast<const P*>(beta), eps,
+                     static_cast<T*>(Y), ldy, mean, rstd);
+  return hipGetLastError();
+}
+
+// One wave to a row while a thread holds at most 4 pieces (nothing to wait for but the wave itself),
+// four waves above that.
+template <class T, class P>
+hipError_t dispatch_forward(const void* X, int M, int K, int ldx, const void* gamma, const void* beta, float eps, void* Y,
+                            int ldy, float* mean, float* rstd, hipStream_t st) {
+  constexpr int W = 64 * VEC<T>;
+#define W4A4_NF(wpr, c) return forward<T, P, wpr, c, 4>(X, M, K, ldx, gamma, beta, eps, Y, ldy, mean, rstd, st)
+  if (K <= W) W4A4_NF(1, 1);
+  if (K <= 2 * W) W4A4_NF(1, 2);
+  if (K <= 4 * W) W4A4_NF(1, 4);
+  if (K <= 8 * W) W4A4_NF(4, 2);
+  if (K <= 16 * W) W4A4_NF(4, 4);
+  if (K <= 32 * W) W4A4_NF(4, 8);
+  if constexpr (sizeof(T) == 4)
+    if (K <= 64 * W) W4A4_NF(4, 16);
+  W4A4_NF(4, 0);
+#undef W4A4_NF
+}
+
+template <class T, class P, int WPR, int C, int WAVES>
+hipError_t backward(const void* dY, int lddy, const void* X, int ldx, const void* gamma, const float* mean,
+                    const float* rstd, int M, int K, void* dX, int lddx, float* dgamma, float* dbeta, float* part,
+                    hipStream_t st) {
+  constexpr int G = WAVES / WPR;
+  const T *dy = static_cast<const T*>(dY), *x = static_cast<const T*>(X);
+  const bool grads = dgamma || dbeta;
+  const int need = (M + G - 1) / G;
+  if (C == 0) {
+    hipLaunchKernelGGL((norm_backward_kernel<T, P, WPR, C, WAVES, false>), dim3(need < 65535 ? need : 65535), dim3(64 * WAVES), 0, st,
+                       dy, lddy, x, ldx, static_cast<const P*>(gamma), mean, rstd, M, K, static_cast<T*>(dX), lddx, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !grads) return e;
+    const int ry = M < 4 * 64 ? (M + 3) / 4 : 64;
+    hipLaunchKernelGGL((norm_columns_kernel<T>), dim3((K + 63) / 64, ry), dim3(256), 0, st, dy, lddy, x, ldx, mean, rstd, M, K, part);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 63) / 64), dim3(1024), 0, st, part, ry, K, dgamma, dbeta);
+    return hipGetLastError();
+  }
+  const int blocks = need < NORM_BLOCKS ? need : NORM_BLOCKS;
+  if (!grads) {
+    hipLaunchKernelGGL((norm_backward_kernel<T, P, WPR, C, WAVES, false>), dim3(blocks), dim3(64 * WAVES), 0, st, dy, lddy, x,
+                       ldx, static_cast<const P*>(gamma), mean, rstd, M, K, static_cast<T*>(dX), lddx, part);
+    return hipGetLastError();
+  }
+  const size_t lds = (size_t)2 * K * sizeof(float);
+  if (lds > 32768) {   // longer rows: allow the block more than the default's dynamic LDS
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&norm_backward_kernel<T, P, WPR, C, WAVES, true>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, 2 * NORM_MAX_K * 4);
+    if (attr != hipSuccess) return attr;
+  }
+  hipLaunchKernelGGL((norm_backward_kernel<T, P, WPR, C, WAVES, true>), dim3(blocks), dim3(64 * WAVES), lds, st, dy, lddy, x, ldx,
+                     static_cast<const P*>(gamma), mean, rstd, M, K, static_cast<T*>(dX), lddx, part);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 63) / 64), dim3(1024), 0, st, part, blocks, K, dgamma, dbeta);
+  return hipGetLastError();
+}
+
+// Row groups of 1, 4 and 16 waves: a thread holds two rows' pieces (the current and the next) and the
+// sums of its columns, so at most 2 (16-bit) or 4 (32-bit) pieces keep it in its registers.
+template <class T, class P>
+hipError_t dispatch_backward(const void* dY, int lddy, const void* X, int ldx, const void* gamma, const float* mean,
+                             const float* rstd, int M, int K, void* dX, int lddx, float* dgamma, float* dbeta, float* part,
+                             hipStream_t st) {
+  constexpr int W = 64 * VEC<T>;
+#define W4A4_NB(wpr, c, waves) \
+  return backward<T, P, wpr, c, waves>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st)
+  if (K <= W) W4A4_NB(1, 1, 16);
+  if (K <= 4 * W) W4A4_NB(4, 1, 16);
+  if (K <= 8 * W) W4A4_NB(4, 2, 16);
+  if (K <= 16 * W) W4A4_NB(16, 1, 16);
+  if (K <= 32 * W) W4A4_NB(16, 2, 16);
+  if constexpr (sizeof(T) == 4)
+    if (K <= 64 * W) W4A4_NB(16, 4, 16);
+  W4A4_NB(4, 0, 4);
+#undef W4A4_NB
+}
+
+bool norm_shape_ok(int M, int K) { return M >= 1 && K >= 1 && M <= (1 << 30) && K <= (1 << 26); }
+bool dtype_ok(int d) { return d == W4A4_DTYPE_BF16 || d == W4A4_DTYPE_F32; }
+bool element_aligned(const void* p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == W4A4_DTYPE_F32 ? 3u : 1u)) == 0; }
+
+}  // namespace
+
+// ================================================================================ C ABI (device)
+extern "C" {
+
+w4a4_status_t w4a4_layer_norm(const void* X, int M, int K, int ldx, int dtype, const void* gamma, const void* beta,
+                              int param_dtype, float eps, void* Y, int ldy, float* mean, float* rstd,
+                              w4a4_stream_t stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return W4A4_ERR_UNSUPPORTED;
+  if (!norm_shape_ok(M, K) || ldx < K || ldy < K || !(eps >= 0.f)) return W4A4_ERR_INVALID_ARG;
+  if (!X || !Y || !mean || !rstd) return W4A4_ERR_INVALID_ARG;
+  if (!element_aligned(X, dtype) || !element_aligned(Y, dtype) || !element_aligned(gamma, param_dtype) ||
+      !element_aligned(beta, param_dtype) || !element_aligned(mean, W4A4_DTYPE_F32) || !element_aligned(rstd, W4A4_DTYPE_F32))
+    return W4A4_ERR_INVALID_ARG;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool p32 = param_dtype == W4A4_DTYPE_F32;
+  hipError_t e;
+  if (dtype == W4A4_DTYPE_BF16)
+    e = p32 ? dispatch_forward<uint16_t, float>(X, M, K, ldx, gamma, beta, eps, Y, ldy, mean, rstd, st)
+            : dispatch_forward<uint16_t, uint16_t>(X, M, K, ldx, gamma, beta, eps, Y, ldy, mean, rstd, st);
+  else
+    e = p32 ? dispatch_forward<float, float>(X, M, K, ldx, gamma, beta, eps, Y, ldy, mean, rstd, st)
+            : dispatch_forward<float, uint16_t>(X, M, K, ldx, gamma, beta, eps, Y, ldy, mean, rstd, st);
+  return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+size_t w4a4_layer_norm_backward_bytes(int M, int K) {
+  if (!norm_shape_ok(M, K)) return 0;
+  const int rows = M < NORM_BLOCKS ? M : NORM_BLOCKS;
+  return (size_t)rows * 2 * (size_t)K * sizeof(float);
+}
+
+w4a4_status_t w4a4_layer_norm_backward(const void* dY, int lddy, const void* X, int ldx, int dtype, const void* gamma,
+                                       int param_dtype, const float* mean, const float* rstd, int M, int K, void* dX,
+                                       int lddx, float* dgamma, float* dbeta, void* ws, w4a4_stream_t stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(param_dtype)) return W4A4_ERR_UNSUPPORTED;
+  if (!norm_shape_ok(M, K) || ldx < K || lddy < K || lddx < K) return W4A4_ERR_INVALID_ARG;
+  if (!dY || !X || !mean || !rstd || !dX || ((dgamma || dbeta) && !ws)) return W4A4_ERR_INVALID_ARG;
+  if (!element_aligned(X, dtype) || !element_aligned(dY, dtype) || !element_aligned(dX, dtype) ||
+      !element_aligned(gamma, param_dtype) || !element_aligned(mean, W4A4_DTYPE_F32) ||
+      !element_aligned(rstd, W4A4_DTYPE_F32) || !element_aligned(dgamma, W4A4_DTYPE_F32) ||
+      !element_aligned(dbeta, W4A4_DTYPE_F32) || !element_aligned(ws, W4A4_DTYPE_F32))
+    return W4A4_ERR_INVALID_ARG;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool p32 = param_dtype == W4A4_DTYPE_F32;
+  float* part = static_cast<float*>(ws);
+  hipError_t e;
+  if (dtype == W4A4_DTYPE_BF16)
+    e = p32 ? dispatch_backward<uint16_t, float>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st)
+            : dispatch_backward<uint16_t, uint16_t>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st);
+  else
+    e = p32 ? dispatch_backward<float, float>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st)
+            : dispatch_backward<float, uint16_t>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st);
+  return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+}
+
+}  // extern "C"
