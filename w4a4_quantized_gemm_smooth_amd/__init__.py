@@ -14,6 +14,7 @@ The library fails loudly when it is missing: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -390,22 +391,54 @@ def gelu_quant_xl1_bytes(M: int, N: int, rank2: int) -> int:
 
 
 # ------------------------------------------------------------- single tokens and training calls
+# These calls take a few microseconds on the GPU for a single token, so their checks are one expression
+# where everything is in order; only where it is not, the refusal is looked for.
 def _check_tensor(name, t, dtype, shape, device, contiguous=True):
     """A tensor of a given type and shape on ``device``: contiguous, or a matrix of any row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and (
+                t.is_contiguous() or not contiguous and t.stride(1) == 1 and t.stride(0) >= shape[1]):
+            return
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
     if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif shape[1] > 1 and t.stride(1) != 1 or shape[0] > 1 and t.stride(0) < shape[1]:
+        raise ValueError(f"{name} must be contiguous")
+    if shape[1] > 1 and t.stride(1) != 1 or shape[0] > 1 and t.stride(0) < shape[1]:
         raise ValueError(f"{name} must have unit stride along its last dimension and rows that do not overlap")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on {device if device.type == 'cuda' else 'a GPU'} (got {t.device})")
+
+
+def _check_bytes(name, t, nbytes, device):
+    """A contiguous device buffer of at least ``nbytes`` bytes (None allowed when 0 are needed)."""
+    if t is None and nbytes == 0:
+        return
+    try:
+        if t.nbytes >= nbytes and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check_buffer(name, t, nbytes, device)
+
+
+def _matrix(name, t):
+    """Shape and device of the matrix that a call's other arguments go by; the kernels are launched on the
+    current device, so it has to be there."""
+    import torch
+    try:
+        M, K = t.shape
+        dev = t.device
+    except (AttributeError, ValueError):
+        raise ValueError(f"{name} must be a 2-D tensor") from None
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (got {dev})")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return M, K, dev
 
 
 def _ld(t):
@@ -413,16 +446,26 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _matrix_shape(name, t):
-    if getattr(t, "ndim", 0) != 2:
-        raise ValueError(f"{name} must be a 2-D tensor")
-    return t.shape
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
+def _queue(stream, dev):
+    """The given stream's handle, or that of the device's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=4096)
 def _two_sizes(fn, *args):
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
     _check(fn, getattr(lib(), fn)(*args, ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(fn, *args):
+    return int(getattr(lib(), fn)(*args))
 
 
 def matvec_sizes(M: int, N: int, K: int, rank: int, fmt=FMT_INT4_G64) -> dict:
@@ -436,14 +479,14 @@ def matvec_weights(codes, scales, N, K, fmt, wv, stream=None):
     as ``matvec`` reads them; all on the GPU."""
     import torch
     f = _fmt(fmt)
-    dev = getattr(wv, "device", torch.device("cpu"))
+    _, _, dev = _matrix("codes", codes)
     _check_tensor("codes", codes, torch.uint8, (N, K // 2), dev)
     if f == FMT_INT4_G64:
         _check_tensor("scales", scales, torch.bfloat16, (N, K // GROUP), dev)
     else:
         _check_tensor("scales", scales, torch.uint8, (N, K // MX_BLOCK), dev)
-    _check_buffer("wv", wv, matvec_sizes(1, N, K, 0, f)["wv"], dev)
-    _check("w4a4_matvec_weights", lib().w4a4_matvec_weights(_dptr(codes), _dptr(scales), N, K, f, _dptr(wv), _stream(stream)))
+    _check_bytes("wv", wv, matvec_sizes(1, N, K, 0, f)["wv"], dev)
+    _check("w4a4_matvec_weights", lib().w4a4_matvec_weights(_ptr(codes), _ptr(scales), N, K, f, _ptr(wv), _queue(stream, dev)))
 
 
 def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=None):
@@ -451,18 +494,21 @@ def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=Non
     4-bit products, the low-rank branch and the bias; two kernels). ``wv`` from ``matvec_weights``."""
     import torch
     f = _fmt(fmt)
-    M = _matrix_shape("x", x)[0]
-    dev = x.device
+    M, _, dev = _matrix("x", x)
     wv_bytes, ws_bytes = _two_sizes("w4a4_matvec_sizes", M, N, K, rank, f)
     _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
     _check_tensor("y", y, torch.bfloat16, (M, N), dev, False)
     rp = (rank + RANK_ALIGN - 1) // RANK_ALIGN * RANK_ALIGN
-    for name, t, n in (("inv_lambda", inv_lambda, 4 * K), ("wv", wv, wv_bytes), ("ws", ws, ws_bytes), ("l1t", l1t, 2 * rp * K),
-                       ("l2t", l2t, 2 * rp * N), ("bias", bias, 0 if bias is None else 2 * N)):
-        _check_buffer(name, t, n, dev)
+    _check_bytes("inv_lambda", inv_lambda, 4 * K, dev)
+    _check_bytes("wv", wv, wv_bytes, dev)
+    _check_bytes("ws", ws, ws_bytes, dev)
+    _check_bytes("l1t", l1t, 2 * rp * K, dev)
+    _check_bytes("l2t", l2t, 2 * rp * N, dev)
+    if bias is not None:
+        _check_bytes("bias", bias, 2 * N, dev)
     _check("w4a4_matvec", lib().w4a4_matvec(
-        _dptr(x), M, K, _ld(x), _dptr(inv_lambda), _dptr(l1t), _dptr(wv), _dptr(l2t), _dptr(bias), _dptr(y), _ld(y), N, rank, f,
-        _dptr(ws), _stream(stream)))
+        _ptr(x), M, K, _ld(x), _ptr(inv_lambda), _ptr(l1t), _ptr(wv), _ptr(l2t), _ptr(bias), _ptr(y), _ld(y), N, rank, f,
+        _ptr(ws), _queue(stream, dev)))
 
 
 def _dtype(t, name):
@@ -486,28 +532,28 @@ def layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=None):
     """y = (x - mean) rstd gamma + beta over the rows of x [M, K] (bf16 or fp32; gamma, beta [K] bf16, fp32
     or None), with the rows' mean and rstd [M] fp32 for ``layer_norm_backward``."""
     import torch
-    M, K = _matrix_shape("x", x)
-    dev, dt = x.device, _dtype(x, "x")
+    M, K, dev = _matrix("x", x)
+    dt = _dtype(x, "x")
     _check_tensor("x", x, x.dtype, (M, K), dev, False)
     _check_tensor("y", y, x.dtype, (M, K), dev, False)
     _check_tensor("mean", mean, torch.float32, (M,), dev)
     _check_tensor("rstd", rstd, torch.float32, (M,), dev)
     pt = _norm_params(gamma, beta, K, dev)
     _check("w4a4_layer_norm", lib().w4a4_layer_norm(
-        _dptr(x), M, K, _ld(x), dt, _dptr(gamma), _dptr(beta), pt, eps, _dptr(y), _ld(y), _dptr(mean), _dptr(rstd),
-        _stream(stream)))
+        _ptr(x), M, K, _ld(x), dt, _ptr(gamma), _ptr(beta), pt, eps, _ptr(y), _ld(y), _ptr(mean), _ptr(rstd),
+        _queue(stream, dev)))
 
 
 def layer_norm_backward_bytes(M: int, K: int) -> int:
-    return int(lib().w4a4_layer_norm_backward_bytes(M, K))
+    return _bytes("w4a4_layer_norm_backward_bytes", M, K)
 
 
 def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
     """dx, and dgamma, dbeta [K] fp32 (either may be None; ``ws`` may be None where both are), of
     ``layer_norm`` from dy, x and the forward pass's mean and rstd."""
     import torch
-    M, K = _matrix_shape("x", x)
-    dev, dt = x.device, _dtype(x, "x")
+    M, K, dev = _matrix("x", x)
+    dt = _dtype(x, "x")
     for name, t in (("dy", dy), ("x", x), ("dx", dx)):
         _check_tensor(name, t, x.dtype, (M, K), dev, False)
     _check_tensor("mean", mean, torch.float32, (M,), dev)
@@ -516,10 +562,10 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=
         if t is not None:
             _check_tensor(name, t, torch.float32, (K,), dev)
     pt = _norm_params(gamma, None, K, dev)
-    _check_buffer("ws", ws, 0 if dgamma is None and dbeta is None else layer_norm_backward_bytes(M, K), dev)
+    _check_bytes("ws", ws, 0 if dgamma is None and dbeta is None else layer_norm_backward_bytes(M, K), dev)
     _check("w4a4_layer_norm_backward", lib().w4a4_layer_norm_backward(
-        _dptr(dy), _ld(dy), _dptr(x), _ld(x), dt, _dptr(gamma), pt, _dptr(mean), _dptr(rstd), M, K, _dptr(dx), _ld(dx),
-        _dptr(dgamma), _dptr(dbeta), _dptr(ws), _stream(stream)))
+        _ptr(dy), _ld(dy), _ptr(x), _ld(x), dt, _ptr(gamma), pt, _ptr(mean), _ptr(rstd), M, K, _ptr(dx), _ld(dx),
+        _ptr(dgamma), _ptr(dbeta), _ptr(ws), _queue(stream, dev)))
 
 
 def checkpoint_sizes(M: int, K: int) -> dict:
@@ -530,47 +576,46 @@ def checkpoint_sizes(M: int, K: int) -> dict:
 
 def _check_checkpoint(codes, scales, M, K, dev):
     c, s = _two_sizes("w4a4_checkpoint_sizes", M, K)
-    _check_buffer("codes", codes, c, dev)
-    _check_buffer("scales", scales, s, dev)
+    _check_bytes("codes", codes, c, dev)
+    _check_bytes("scales", scales, s, dev)
 
 
 def checkpoint_pack(x, codes, scales, stream=None):
     """Keep x [M, K] bf16 in 8 bits: int8 codes and a power-of-two scale per channel and 32 tokens."""
     import torch
-    M, K = _matrix_shape("x", x)
-    _check_tensor("x", x, torch.bfloat16, (M, K), x.device, False)
-    _check_checkpoint(codes, scales, M, K, x.device)
+    M, K, dev = _matrix("x", x)
+    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
+    _check_checkpoint(codes, scales, M, K, dev)
     _check("w4a4_checkpoint_pack", lib().w4a4_checkpoint_pack(
-        _dptr(x), M, K, _ld(x), _dptr(codes), _dptr(scales), _stream(stream)))
+        _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _queue(stream, dev)))
 
 
 def checkpoint_unpack(codes, scales, x, stream=None):
     """What the codes and scales stand for, into x [M, K] bf16 (exact)."""
     import torch
-    M, K = _matrix_shape("x", x)
-    _check_tensor("x", x, torch.bfloat16, (M, K), x.device, False)
-    _check_checkpoint(codes, scales, M, K, x.device)
+    M, K, dev = _matrix("x", x)
+    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
+    _check_checkpoint(codes, scales, M, K, dev)
     _check("w4a4_checkpoint_unpack", lib().w4a4_checkpoint_unpack(
-        _dptr(codes), _dptr(scales), M, K, _dptr(x), _ld(x), _stream(stream)))
+        _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x), _queue(stream, dev)))
 
 
 def checkpoint_weight_grad_bytes(M: int, N: int, K: int) -> int:
-    return int(lib().w4a4_checkpoint_weight_grad_bytes(M, N, K))
+    return _bytes("w4a4_checkpoint_weight_grad_bytes", M, N, K)
 
 
 def checkpoint_weight_grad(dy, codes, scales, K, dw, ws, stream=None):
     """dw [N, K] (fp32 or bf16) = dy^T x for dy [M, N] bf16 and the activations [M, K] kept in (codes,
     scales)."""
     import torch
-    M, N = _matrix_shape("dy", dy)
-    dev = dy.device
+    M, N, dev = _matrix("dy", dy)
     _check_tensor("dy", dy, torch.bfloat16, (M, N), dev, False)
     _check_checkpoint(codes, scales, M, K, dev)
     dt = _dtype(dw, "dw")
     _check_tensor("dw", dw, dw.dtype, (N, K), dev)
-    _check_buffer("ws", ws, checkpoint_weight_grad_bytes(M, N, K), dev)
+    _check_bytes("ws", ws, checkpoint_weight_grad_bytes(M, N, K), dev)
     _check("w4a4_checkpoint_weight_grad", lib().w4a4_checkpoint_weight_grad(
-        _dptr(dy), _ld(dy), _dptr(codes), _dptr(scales), M, N, K, _dptr(dw), dt, _dptr(ws), _stream(stream)))
+        _ptr(dy), _ld(dy), _ptr(codes), _ptr(scales), M, N, K, _ptr(dw), dt, _ptr(ws), _queue(stream, dev)))
 
 
 def _act(act) -> int:
@@ -581,41 +626,44 @@ def _act(act) -> int:
 
 def _check_gated(x, wg, wu, h, name):
     import torch
-    M, K = _matrix_shape("x", x)
-    F = _matrix_shape("wg", wg)[0]
-    for n, t, shape in (("x", x, (M, K)), ("wg", wg, (F, K)), ("wu", wu, (F, K)), (name, h, (M, F))):
-        _check_tensor(n, t, torch.bfloat16, shape, x.device, False)
+    M, K, dev = _matrix("x", x)
+    F = _matrix("wg", wg)[0]
+    bf16 = torch.bfloat16
+    _check_tensor("x", x, bf16, (M, K), dev, False)
+    _check_tensor("wg", wg, bf16, (F, K), dev, False)
+    _check_tensor("wu", wu, bf16, (F, K), dev, False)
+    _check_tensor(name, h, bf16, (M, F), dev, False)
     if _ld(wg) != _ld(wu):
         raise ValueError("wg and wu must have the same row stride")
-    return M, K, F
+    return M, K, F, dev
 
 
 def gated_forward_bytes(M: int, K: int, F: int) -> int:
-    return int(lib().w4a4_gated_forward_bytes(M, K, F))
+    return _bytes("w4a4_gated_forward_bytes", M, K, F)
 
 
 def gated_forward(x, wg, wu, act, h, ws=None, stream=None):
     """h [M, F] = act(x wg^T) * (x wu^T) for x [M, K], wg and wu [F, K], bf16; act "silu" or "gelu"."""
-    M, K, F = _check_gated(x, wg, wu, h, "h")
-    _check_buffer("ws", ws, gated_forward_bytes(M, K, F), x.device)
+    M, K, F, dev = _check_gated(x, wg, wu, h, "h")
+    _check_bytes("ws", ws, gated_forward_bytes(M, K, F), dev)
     _check("w4a4_gated_forward", lib().w4a4_gated_forward(
-        _dptr(x), M, K, _ld(x), _dptr(wg), _dptr(wu), _ld(wg), F, _act(act), _dptr(h), _ld(h), _dptr(ws), _stream(stream)))
+        _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(h), _ld(h), _ptr(ws), _queue(stream, dev)))
 
 
 def gated_backward_bytes(M: int, K: int, F: int) -> int:
-    return int(lib().w4a4_gated_backward_bytes(M, K, F))
+    return _bytes("w4a4_gated_backward_bytes", M, K, F)
 
 
 def gated_backward(dh, x, wg, wu, act, dx, dwg, dwu, ws, stream=None):
     """dx [M, K], dwg and dwu [F, K] (bf16) of ``gated_forward`` from dh [M, F] and its inputs."""
     import torch
-    M, K, F = _check_gated(x, wg, wu, dh, "dh")
+    M, K, F, dev = _check_gated(x, wg, wu, dh, "dh")
     for n, t, shape in (("dx", dx, (M, K)), ("dwg", dwg, (F, K)), ("dwu", dwu, (F, K))):
-        _check_tensor(n, t, torch.bfloat16, shape, x.device)
-    _check_buffer("ws", ws, gated_backward_bytes(M, K, F), x.device)
+        _check_tensor(n, t, torch.bfloat16, shape, dev)
+    _check_bytes("ws", ws, gated_backward_bytes(M, K, F), dev)
     _check("w4a4_gated_backward", lib().w4a4_gated_backward(
-        _dptr(dh), _ld(dh), _dptr(x), M, K, _ld(x), _dptr(wg), _dptr(wu), _ld(wg), F, _act(act), _dptr(dx), _dptr(dwg),
-        _dptr(dwu), _dptr(ws), _stream(stream)))
+        _ptr(dh), _ld(dh), _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(dx), _ptr(dwg),
+        _ptr(dwu), _ptr(ws), _queue(stream, dev)))
 
 
 class W4A4Linear:

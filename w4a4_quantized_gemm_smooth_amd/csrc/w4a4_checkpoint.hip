@@ -23,6 +23,8 @@ namespace {
 constexpr int CK_CH = 4;        // channels per thread
 constexpr int CK_THREADS = 256;
 
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ float half_of(uint32_t w, int hi) { return __uint_as_float(hi ? (w & 0xFFFF0000u) : (w << 16)); }
 
 // 2^e from its byte; byte 0 is the subnormal 2^-127, 255 NaN
@@ -42,31 +44,42 @@ __global__ __launch_bounds__(CK_THREADS) void checkpoint_pack_kernel(const uint1
 #pragma unroll
   for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r)
     v[r] = r < rows ? *reinterpret_cast<const uint2*>(x + (size_t)r * ldx) : uint2{0u, 0u};
+  // the largest magnitudes' bits, two channels to a word (magnitudes order as their bits do, NaN last)
+  us2 tx = {0, 0}, ty = {0, 0};
+#pragma unroll
+  for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r) {
+    tx = __builtin_elementwise_max(tx, __builtin_bit_cast(us2, v[r].x & 0x7FFF7FFFu));
+    ty = __builtin_elementwise_max(ty, __builtin_bit_cast(us2, v[r].y & 0x7FFF7FFFu));
+  }
   uint32_t bytes = 0u;
   uint4* out = reinterpret_cast<uint4*>(codes + ((size_t)b * K + k) * W4A4_CHECKPOINT_BLOCK);
 #pragma unroll
   for (int c = 0; c < CK_CH; ++c) {
-    uint32_t top = 0u;   // the largest magnitude's bits (magnitudes order as their bits do, NaN last)
-#pragma unroll
-    for (int r = 0; r < W4A4_CHECKPOINT_BLOCK; ++r)
-      top = max(top, ((c < 2 ? v[r].x : v[r].y) >> (16 * (c & 1))) & 0x7FFFu);
+    const uint32_t top = c < 2 ? tx[c & 1] : ty[c & 1];
     // a = 1.m 2^(t-127): 127 2^e >= a from e = t - 133 on where 1.m <= 127/64 (m <= 126 of 128)
     const int t = (int)(top >> 7), e = max(0, t - 6 + ((top & 127u) > 126u ? 1 : 0));
     const bool bad = t == 255;
     bytes |= (uint32_t)(bad ? 255 : e) << (8 * c);
-    const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);   // 2^-(e - 127); e <= 249
-    const float most = e == 249 ? 63.f : 127.f;
+    const float inv = __uint_as_float((uint32_t)(254 - min(e, 249)) << 23);   // 2^-(e - 127)
     uint32_t w[8];
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
-      uint32_t word = 0u;
+      uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * d + i;
-        const float y = fminf(most, fmaxf(-most, __builtin_rintf(half_of(c < 2 ? v[r].x : v[r].y, c & 1) * inv)));
-        word |= ((uint32_t)(bad ? 0 : (int)y) & 0xFFu) << (8 * i);
+      for (int i = 0; i < 4; ++i)   // x 2^-e rounded to a whole number: the last byte of 1.5 2^23 + x 2^-e
+        y[i] = __float_as_uint(fmaf(half_of(c < 2 ? v[4 * d + i].x : v[4 * d + i].y, c & 1), inv, 12582912.f));
+      w[d] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(y[3], y[2], 0x0c0c0400u), __builtin_amdgcn_perm(y[1], y[0], 0x0c0c0400u), 0x05040100u);
+    }
+    if (bad || e == 249) {   // rare: no codes, or none beyond 63
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t word = 0u;
+        for (int i = 0; i < 4; ++i) {
+          const int q = (int)(int8_t)(w[d] >> (8 * i));
+          word |= ((uint32_t)(bad ? 0 : max(-63, min(63, q))) & 0xFFu) << (8 * i);
+        }
+        w[d] = word;
       }
-      w[d] = word;
     }
     out[2 * c] = uint4{w[0], w[1], w[2], w[3]};
     out[2 * c + 1] = uint4{w[4], w[5], w[6], w[7]};

@@ -17,10 +17,10 @@
 // (r = lane % 16, j = lane / 16) holds the codes k = 64 (2p + d/2) + 32 (d % 2) + 8 j + 0..7 of row r.
 // After all codes: per tile, pair and row a dword of scales (two bf16, or four E8M0 bytes).
 //
-// Work split: a block of 8 waves takes 128 rows of W and a slice of K; x^ of the slice is made once a
-// block, in LDS; a wave takes 16 rows and issues all its loads of codes before that. A second kernel
-// adds the slices in slice order and the low-rank branch, whose down projection t runs in blocks of
-// its own beside the first kernel's others.
+// Work split: a block of 8 waves takes 8 or 16 tiles of W and a slice of K; x^ of the slice is made once a
+// block, in LDS; a wave takes one or two tiles and issues all its loads of codes before that. The down
+// projection t runs in blocks of its own beside those, 16 ranks and 2048 of K each. A second kernel adds
+// the slices in slice order, t L2 and the bias.
 #include "w4a4_device_common.h"
 
 using namespace w4a4;
@@ -28,16 +28,23 @@ using namespace w4a4::dev;
 
 namespace {
 
-constexpr int MV_WAVES = 8, MV_THREADS = 64 * MV_WAVES, MV_ROWS = 16 * MV_WAVES;  // rows of W a block
+constexpr int MV_WAVES = 8, MV_THREADS = 64 * MV_WAVES;
 constexpr int MV_MAX_M = W4A4_MATVEC_MAX_ROWS;
+constexpr int MV_TK = 2048;      // K of a block of the down projection: 256 a wave
+#ifndef W4A4_MV_TARGET           // build-time tuning knob: blocks aimed at
+#define W4A4_MV_TARGET 512
+#endif
 
 inline int mv_tiles(int N) { return (N + 15) / 16; }
 inline int mv_pairs(int K) { return (K + 2 * W4A4_GROUP - 1) / (2 * W4A4_GROUP); }
-inline int mv_blocks(int N) { return (N + MV_ROWS - 1) / MV_ROWS; }
-// pairs of groups a slice: the longest slice that still gives two blocks to each compute unit
-inline int mv_slice(int N, int K) {
+inline int mv_tslices(int K) { return (K + MV_TK - 1) / MV_TK; }
+// tiles a wave: two (x^ made and read for twice the rows) where that still leaves enough blocks
+inline int mv_nt(int M, int N) { return M > 8 && N >= 2048 ? 2 : 1; }
+inline int mv_blocks(int M, int N) { return (mv_tiles(N) + MV_WAVES * mv_nt(M, N) - 1) / (MV_WAVES * mv_nt(M, N)); }
+// pairs of groups a slice: the longest slice that still gives the grid its blocks
+inline int mv_slice(int M, int N, int K) {
   for (int sp = 8; sp > 1; sp /= 2)
-    if (mv_blocks(N) * ((mv_pairs(K) + sp - 1) / sp) >= 512) return sp;
+    if (mv_blocks(M, N) * ((mv_pairs(K) + sp - 1) / sp) >= W4A4_MV_TARGET) return sp;
   return 1;
 }
 
@@ -87,45 +94,55 @@ __global__ __launch_bounds__(256) void matvec_weights_kernel(const uint8_t* __re
 }
 
 // ---------------------------------------------------------------------------------- main kernel
-// x^ of the block's slice -> LDS: rows 0..M-1 hi, M..2M-1 lo, row 2M zeros, of `stride` bytes (a
+// 8 activations from x and 1/lambda, as hi and lo
+__device__ __forceinline__ void split_x(const uint16_t* __restrict__ x, const float* __restrict__ inv, uint32_t (&hi)[4],
+                                        uint32_t (&lo)[4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(x);
+  const float4 a = *reinterpret_cast<const float4*>(inv), b = *reinterpret_cast<const float4*>(inv + 4);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float il[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const float x0 = __uint_as_float(w[d] << 16) * il[2 * d], x1 = __uint_as_float(w[d] & 0xFFFF0000u) * il[2 * d + 1];
+    hi[d] = pack_bf16x2(x0, x1);
+    lo[d] = pack_bf16x2(x0 - __uint_as_float(hi[d] << 16), x1 - __uint_as_float(hi[d] & 0xFFFF0000u));
+  }
+}
+__device__ __forceinline__ float sum8(const uint32_t (&v)[4]) {
+  float s = 0.f;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) s += __uint_as_float(v[d] << 16) + __uint_as_float(v[d] & 0xFFFF0000u);
+  return s;
+}
+
+// x^ of the block's slice -> LDS: rows 0..M-1 hi, M..2M-1 lo, row 2M zeros, of SP * 256 + 64 bytes (a
 // multiple of 64 not of 128: 16-byte reads of 16 rows x 4 chunks then meet each bank equally often);
 // and -24 times the group sums, [2 SP][16], by the row of the matrix operand. K and beyond: zeros.
-template <int SP>
+template <int SP, bool TWO, bool SUMS>
 __device__ __forceinline__ void stage_x(const uint16_t* __restrict__ X, int ldx, const float* __restrict__ inv, int M, int K,
-                                        int kbase, uint8_t* xs, float* sums, bool two) {
+                                        int kbase, uint8_t* xs, float* sums) {
   constexpr int STRIDE = SP * 256 + 64, CH = SP * 16;
-  for (int i = threadIdx.x; i < 2 * SP * 16; i += MV_THREADS) sums[i] = 0.f;
+  if (SUMS)
+    for (int i = threadIdx.x; i < 2 * SP * 16; i += MV_THREADS)
+      if ((TWO ? i & 15 : i & 7) >= M) sums[i] = 0.f;
   for (int i = threadIdx.x; i < CH; i += MV_THREADS) *reinterpret_cast<uint4*>(xs + 2 * M * STRIDE + 16 * i) = uint4{0u, 0u, 0u, 0u};
-  __syncthreads();
   for (int i = threadIdx.x; i < M * CH; i += MV_THREADS) {
     const int m = i / CH, c = i % CH, k = kbase + 8 * c;
     uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-    float sh = 0.f, sl = 0.f;
-    if (k < K) {   // K is a multiple of 64
-      const uint4 v = *reinterpret_cast<const uint4*>(X + (size_t)m * ldx + k);
-      const float4 a = *reinterpret_cast<const float4*>(inv + k), b = *reinterpret_cast<const float4*>(inv + k + 4);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      const float il[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const float x0 = __uint_as_float(w[d] << 16) * il[2 * d], x1 = __uint_as_float(w[d] & 0xFFFF0000u) * il[2 * d + 1];
-        hi[d] = pack_bf16x2(x0, x1);
-        const float h0 = __uint_as_float(hi[d] << 16), h1 = __uint_as_float(hi[d] & 0xFFFF0000u);
-        lo[d] = pack_bf16x2(x0 - h0, x1 - h1);
-        sh += h0 + h1;
-        sl += __uint_as_float(lo[d] << 16) + __uint_as_float(lo[d] & 0xFFFF0000u);
-      }
-    }
+    if (k < K) split_x(X + (size_t)m * ldx + k, inv + k, hi, lo);   // K is a multiple of 64
     *reinterpret_cast<uint4*>(xs + m * STRIDE + 16 * c) = uint4{hi[0], hi[1], hi[2], hi[3]};
     *reinterpret_cast<uint4*>(xs + (M + m) * STRIDE + 16 * c) = uint4{lo[0], lo[1], lo[2], lo[3]};
+    if (SUMS) {
+      float sh = sum8(hi), sl = sum8(lo);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {   // the 8 threads of a group (whole or absent: CH is a multiple of 8)
-      sh += __shfl_xor(sh, o);
-      sl += __shfl_xor(sl, o);
-    }
-    if ((c & 7) == 0) {
-      sums[(c >> 3) * 16 + m] = -24.f * (two ? sh + sl : sh);
-      if (!two) sums[(c >> 3) * 16 + 8 + m] = -24.f * sl;
+      for (int o = 1; o < 8; o <<= 1) {   // the 8 threads of a group (whole or absent: CH is a multiple of 8)
+        sh += __shfl_xor(sh, o);
+        sl += __shfl_xor(sl, o);
+      }
+      if ((c & 7) == 0) {
+        sums[(c >> 3) * 16 + m] = -24.f * (TWO ? sh + sl : sh);
+        if (!TWO) sums[(c >> 3) * 16 + 8 + m] = -24.f * sl;
+      }
     }
   }
   __syncthreads();
@@ -135,182 +152,233 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-// TWO: M > 8, the hi and lo rows are two operands. Blocks: index = slice * (nb + tb) + b; b < nb the
-// rows of W, b = nb (where rank > 0) the down projection.
-template <bool MX, bool TWO, int SP>
-__global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __restrict__ X, int ldx,
-                                                            const float* __restrict__ inv, const uint16_t* __restrict__ l1t,
-                                                            const uint8_t* __restrict__ wv, int M, int N, int K, int rp,
-                                                            int nb, float* __restrict__ part, float* __restrict__ tpart) {
-  constexpr int STRIDE = SP * 256 + 64;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  float* sums = reinterpret_cast<float*>(lds);
-  uint8_t* xs = lds + 2 * SP * 16 * 4;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
-  const int per = nb + (rp > 0 ? 1 : 0), slice = blockIdx.x / per, b = blockIdx.x % per;
-  const int G = K / W4A4_GROUP, P = (G + 1) / 2, tiles = (N + 15) / 16, p0 = slice * SP, np = min(SP, P - p0);
-  const int row_hi = TWO ? (r < M ? r : 2 * M) : (r < 8 ? (r < M ? r : 2 * M) : (r - 8 < M ? M + r - 8 : 2 * M));
-  const uint8_t* xh = xs + row_hi * STRIDE + 16 * j;
-  const uint8_t* xl = xs + (r < M ? M + r : 2 * M) * STRIDE + 16 * j;   // TWO only
-
-  if (b == nb) {   // t: 16 rows of L1^T a wave; waves beyond the rank's tiles take other pairs
-    const int rt = rp / 16, nsub = MV_WAVES / rt, tile = wave % rt, sub = wave / rt;
-    stage_x<SP>(X, ldx, inv, M, K, p0 * 128, xs, sums, TWO);
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    if (sub < nsub) {
-      for (int i = sub; i < np; i += nsub)
+// A block of the down projection: ranks 16 tile .. + 15, a slice of MV_TK, -> tpart [slice][M][rp]. Each
+// lane makes its own operand of x^: nothing is shared but the waves' sums at the end.
+template <bool TWO>
+__device__ __forceinline__ void down_block(const uint16_t* __restrict__ X, int ldx, const float* __restrict__ inv,
+                                           const uint16_t* __restrict__ l1t, int M, int K, int rp, int tile, int slice,
+                                           float* red, float* __restrict__ tpart) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, j = lane >> 4;
+  const int m = TWO ? r : r & 7, k0 = slice * MV_TK + wave * (MV_TK / MV_WAVES) + 8 * j;
+  const uint16_t* x = X + (size_t)min(m, M - 1) * ldx;
+  const uint16_t* l = l1t + (size_t)(tile * 16 + r) * K;
+  const v4i zero = {0, 0, 0, 0};
+  v4i w[MV_TK / MV_WAVES / 32];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const int k = (p0 + i) * 128 + 32 * d + 8 * j;
-          const v4i w = k < K ? *reinterpret_cast<const v4i*>(l1t + (size_t)(tile * 16 + r) * K + k) : v4i{0, 0, 0, 0};
-          acc = mfma16(*reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d), w, acc);
-          if (TWO) acc = mfma16(*reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d), w, acc);
-        }
-    }
-    if (!TWO) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[v] += __shfl_xor(acc[v], 32);
-    }
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(xs);   // [waves][16][16]: 8 KB; x^ is done with
-    if (TWO || j < 2) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * j + v) * 16 + r] = acc[v];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < M * rp; i += MV_THREADS) {
-      const int m = i / rp, c = i % rp;
-      float s = 0.f;
-      for (int q = 0; q < nsub; ++q) s += red[((q * rt + c / 16) * 16 + m) * 16 + (c & 15)];
-      tpart[(size_t)slice * M * rp + i] = s;
-    }
-    return;
-  }
-
-  const int tile = b * MV_WAVES + wave;
-  const bool live = tile < tiles;
-  const v4i* cw = reinterpret_cast<const v4i*>(wv) + ((size_t)(live ? tile : 0) * P + p0) * 64 + lane;
-  const uint32_t* sw = reinterpret_cast<const uint32_t*>(wv + (size_t)tiles * P * 1024) + ((size_t)(live ? tile : 0) * P + p0) * 16 + r;
-  v4i w[SP];
-  uint32_t sc[SP];
-#pragma unroll
-  for (int i = 0; i < SP; ++i) {
-    const int q = min(i, np - 1);
-    w[i] = cw[q * 64];
-    sc[i] = sw[q * 16];
-  }
-  stage_x<SP>(X, ldx, inv, M, K, p0 * 128, xs, sums, TWO);
-  if (!live) return;
+  for (int i = 0; i < MV_TK / MV_WAVES / 32; ++i) w[i] = k0 + 32 * i < K ? *reinterpret_cast<const v4i*>(l + k0 + 32 * i) : zero;
   v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < SP; ++i) {
-    if (i >= np) break;
-    v4f pt = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const uint32_t c = (uint32_t)w[i][d];
-      v4i op;
-      if constexpr (MX) {
-        op[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
-        op[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1));
-        op[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2));
-        op[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3));
-        pt = v4f{0.f, 0.f, 0.f, 0.f};
-      } else {
-        op[0] = (int)(((c << 3) & 0x00780078u) | 0x41804180u);
-        op[1] = (int)(((c >> 1) & 0x00780078u) | 0x41804180u);
-        op[2] = (int)(((c >> 5) & 0x00780078u) | 0x41804180u);
-        op[3] = (int)(((c >> 9) & 0x00780078u) | 0x41804180u);
-        if ((d & 1) == 0) pt = *reinterpret_cast<const v4f*>(sums + (2 * i + (d >> 1)) * 16 + 4 * j);
-      }
-      pt = mfma16(*reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d), op, pt);
-      if (TWO) pt = mfma16(*reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d), op, pt);
-      if (MX || (d & 1)) {
-        const float s = MX ? e8m0((sc[i] >> (8 * d)) & 255u) : (d == 1 ? __uint_as_float(sc[i] << 16) : __uint_as_float(sc[i] & 0xFFFF0000u));
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = fmaf(s, pt[v], acc[v]);
-      }
+  for (int i = 0; i < MV_TK / MV_WAVES / 32; ++i) {
+    const int k = k0 + 32 * i;
+    uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+    if (k < K && m < M) split_x(x + k, inv + k, hi, lo);
+    const v4i h = v4i{(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]}, q = v4i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3]};
+    if (TWO) {
+      acc = mfma16(h, w[i], acc);
+      acc = mfma16(q, w[i], acc);
+    } else {
+      acc = mfma16(r < 8 ? h : q, w[i], acc);
     }
   }
   if (!TWO) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] += __shfl_xor(acc[v], 32);
   }
-  float* out = part + (size_t)slice * M * (tiles * 16) + tile * 16 + r;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int m = 4 * j + v;
-    if (m < M && (TWO || j < 2)) out[(size_t)m * (tiles * 16)] = acc[v];
+  for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * j + v) * 16 + r] = acc[v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < M * 16; i += MV_THREADS) {
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < MV_WAVES; ++q) s += red[q * 256 + i];
+    tpart[((size_t)slice * M + (i >> 4)) * rp + tile * 16 + (i & 15)] = s;
   }
 }
 
-// y = the slices' sums + t L2 + bias; a block 64 columns, a wave every fourth row.
-__global__ __launch_bounds__(256) void matvec_finish_kernel(const float* __restrict__ part, const float* __restrict__ tpart,
-                                                            int slices, const uint16_t* __restrict__ l2t,
-                                                            const uint16_t* __restrict__ bias, int M, int N, int rp,
-                                                            uint16_t* __restrict__ Y, int ldy) {
-  __shared__ float t[MV_MAX_M * W4A4_MAX_RANK];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * 64 + lane, np = (N + 15) / 16 * 16;
-  for (int i = threadIdx.x; i < M * rp; i += 256) {
-    float s = 0.f;
-    for (int q = 0; q < slices; ++q) s += tpart[(size_t)q * M * rp + i];
-    t[i] = s;
+// TWO: M > 8, the hi and lo rows are two operands. Blocks 0 .. tb - 1: the down projection; then slice by
+// slice the rows of W.
+template <bool MX, bool TWO, int NT, int SP>
+__global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __restrict__ X, int ldx,
+                                                            const float* __restrict__ inv, const uint16_t* __restrict__ l1t,
+                                                            const uint8_t* __restrict__ wv, int M, int N, int K, int rp,
+                                                            int nb, int tb, float* __restrict__ part,
+                                                            float* __restrict__ tpart) {
+  constexpr int STRIDE = SP * 256 + 64;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* sums = reinterpret_cast<float*>(lds);
+  uint8_t* xs = lds + 2 * SP * 16 * 4;
+  if ((int)blockIdx.x < tb) {
+    down_block<TWO>(X, ldx, inv, l1t, M, K, rp, blockIdx.x % (rp / 16), blockIdx.x / (rp / 16), sums, tpart);
+    return;
   }
-  __syncthreads();
-  if (n >= N) return;
-  float acc[MV_MAX_M / 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
+  const int slice = (blockIdx.x - tb) / nb, b = (blockIdx.x - tb) % nb;
+  const int P = (K / W4A4_GROUP + 1) / 2, tiles = (N + 15) / 16, p0 = slice * SP, np = min(SP, P - p0);
+  const int tile0 = (b * MV_WAVES + wave) * NT;
+  v4i w[NT][SP];
+  uint32_t sc[NT][SP];
 #pragma unroll
-  for (int i = 0; i < MV_MAX_M / 4; ++i) {
-    const int m = w + 4 * i;
-    acc[i] = 0.f;
-    if (m < M)
-      for (int q = 0; q < slices; ++q) acc[i] += part[((size_t)q * M + m) * np + n];
-  }
-  for (int c = 0; c < rp; c += 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(l2t + (size_t)n * rp + c);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  for (int n = 0; n < NT; ++n) {   // tiles and pairs past the end repeat the last one, unused
+    const size_t at = (size_t)min(tile0 + n, tiles - 1) * P + p0;
+    const v4i* cw = reinterpret_cast<const v4i*>(wv) + at * 64 + lane;
+    const uint32_t* sw = reinterpret_cast<const uint32_t*>(wv + (size_t)tiles * P * 1024) + at * 16 + r;
 #pragma unroll
-    for (int i = 0; i < MV_MAX_M / 4; ++i) {
-      const int m = w + 4 * i;
-      if (m >= M) break;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        acc[i] = fmaf(t[m * rp + c + e], __uint_as_float((e & 1) ? (u[e >> 1] & 0xFFFF0000u) : (u[e >> 1] << 16)), acc[i]);
+    for (int i = 0; i < SP; ++i) {
+      const int q = min(i, np - 1);
+      w[n][i] = cw[q * 64];
+      sc[n][i] = sw[q * 16];
     }
   }
-  const float bb = bias ? bf16f(bias[n]) : 0.f;
+  stage_x<SP, TWO, !MX>(X, ldx, inv, M, K, p0 * 128, xs, sums);
+  if (tile0 >= tiles) return;
+  const int row_hi = TWO ? (r < M ? r : 2 * M) : (r < 8 ? (r < M ? r : 2 * M) : (r - 8 < M ? M + r - 8 : 2 * M));
+  const uint8_t* xh = xs + row_hi * STRIDE + 16 * j;
+  const uint8_t* xl = xs + (r < M ? M + r : 2 * M) * STRIDE + 16 * j;   // TWO only
+  v4f acc[NT];
 #pragma unroll
-  for (int i = 0; i < MV_MAX_M / 4; ++i) {
-    const int m = w + 4 * i;
-    if (m < M) Y[(size_t)m * ldy + n] = (uint16_t)pack_bf16x2(acc[i] + bb, 0.f);
+  for (int n = 0; n < NT; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < SP; ++i) {
+    if (i >= np) break;
+    v4f pt[NT];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const v4i h = *reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d);
+      const v4i l = TWO ? *reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d) : v4i{0, 0, 0, 0};
+      v4f start = {0.f, 0.f, 0.f, 0.f};
+      if (!MX && (d & 1) == 0) start = *reinterpret_cast<const v4f*>(sums + (2 * i + (d >> 1)) * 16 + 4 * j);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t c = (uint32_t)w[n][i][d];
+        v4i op;
+        if constexpr (MX) {
+          op[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
+          op[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1));
+          op[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2));
+          op[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3));
+        } else {
+          op[0] = (int)(((c << 3) & 0x00780078u) | 0x41804180u);
+          op[1] = (int)(((c >> 1) & 0x00780078u) | 0x41804180u);
+          op[2] = (int)(((c >> 5) & 0x00780078u) | 0x41804180u);
+          op[3] = (int)(((c >> 9) & 0x00780078u) | 0x41804180u);
+        }
+        pt[n] = mfma16(h, op, MX || (d & 1) == 0 ? start : pt[n]);
+        if (TWO) pt[n] = mfma16(l, op, pt[n]);
+        if (MX || (d & 1)) {
+          const float s = MX ? e8m0((sc[n][i] >> (8 * d)) & 255u)
+                             : (d == 1 ? __uint_as_float(sc[n][i] << 16) : __uint_as_float(sc[n][i] & 0xFFFF0000u));
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[n][v] = fmaf(s, pt[n][v], acc[n][v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (tile0 + n >= tiles) break;
+    if (!TWO) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[n][v] += __shfl_xor(acc[n][v], 32);
+    }
+    float* out = part + (size_t)slice * M * (tiles * 16) + (tile0 + n) * 16 + r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int m = 4 * j + v;
+      if (m < M && (TWO || j < 2)) out[(size_t)m * (tiles * 16)] = acc[n][v];
+    }
   }
 }
 
-template <bool MX, bool TWO, int SP>
-hipError_t launch(const uint16_t* X, int ldx, const float* inv, const uint16_t* l1t, const uint8_t* wv, int M, int N, int K,
-                  int rp, float* part, float* tpart, hipStream_t st) {
-  const int slices = (mv_pairs(K) + SP - 1) / SP, nb = mv_blocks(N);
-  size_t lds = (size_t)2 * SP * 16 * 4 + (size_t)(2 * M + 1) * (SP * 256 + 64);
-  if (lds < 2 * SP * 16 * 4 + 8192) lds = 2 * SP * 16 * 4 + 8192;   // the down projection's sums
+// y = the slices' sums + t L2 + bias. A block takes one row and 128 columns: 32 threads four columns each,
+// eight times over the slices (8 q + g in order, then the eight in order); then two threads a column, half
+// the ranks each.
+__global__ __launch_bounds__(256) void matvec_finish_kernel(const float* __restrict__ part, int slices,
+                                                            const float* __restrict__ tpart, int tslices,
+                                                            const uint16_t* __restrict__ l2t,
+                                                            const uint16_t* __restrict__ bias, int M, int N, int rp,
+                                                            uint16_t* __restrict__ Y, int ldy) {
+  __shared__ float t[W4A4_MAX_RANK];
+  __shared__ __attribute__((aligned(16))) float red[8][128];
+  const int m = blockIdx.y, np = (N + 15) / 16 * 16, tid = threadIdx.x;
+  const int c4 = blockIdx.x * 128 + 4 * (tid & 31), g = tid >> 5;
+  float4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c4 < np) {
+#pragma unroll 4
+    for (int q = g; q < slices; q += 8) {
+      const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)q * M + m) * np + c4);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  const int n = blockIdx.x * 128 + (tid >> 1), half = tid & 1;
+  uint4 l2[W4A4_MAX_RANK / 16];   // this thread's half of the column's ranks, rank_pad / 16 pieces of 8
+#pragma unroll
+  for (int i = 0; i < W4A4_MAX_RANK / 16; ++i)
+    if (16 * i < rp && n < N) l2[i] = *reinterpret_cast<const uint4*>(l2t + (size_t)n * rp + 16 * i + 8 * half);
+  if (tid < rp) {
+    float a = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < tslices; ++q) a += tpart[((size_t)q * M + m) * rp + tid];
+    t[tid] = a;
+  }
+  *reinterpret_cast<float4*>(&red[g][4 * (tid & 31)]) = s;
+  __syncthreads();
+  float a = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a += red[4 * half + q][tid >> 1];
+#pragma unroll
+  for (int i = 0; i < W4A4_MAX_RANK / 16; ++i) {
+    if (16 * i >= rp || n >= N) break;
+    const uint32_t u[4] = {l2[i].x, l2[i].y, l2[i].z, l2[i].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      a = fmaf(t[16 * i + 8 * half + e], __uint_as_float((e & 1) ? (u[e >> 1] & 0xFFFF0000u) : (u[e >> 1] << 16)), a);
+  }
+  a += __shfl_xor(a, 1);
+  if (half == 0 && n < N) Y[(size_t)m * ldy + n] = (uint16_t)pack_bf16x2(a + (bias ? bf16f(bias[n]) : 0.f), 0.f);
+}
+
+struct MatvecArgs {
+  const uint16_t* X;
+  int ldx;
+  const float* inv;
+  const uint16_t* l1t;
+  const uint8_t* wv;
+  int M, N, K, rp;
+  float *part, *tpart;
+};
+
+template <bool MX, bool TWO, int NT, int SP>
+hipError_t launch(const MatvecArgs& a, hipStream_t st) {
+  const int slices = (mv_pairs(a.K) + SP - 1) / SP, nb = mv_blocks(a.M, a.N), tb = a.rp / 16 * mv_tslices(a.K);
+  size_t lds = (size_t)2 * SP * 16 * 4 + (size_t)(2 * a.M + 1) * (SP * 256 + 64);
+  if (lds < MV_WAVES * 1024) lds = MV_WAVES * 1024;   // the down projection's sums
   if (lds > 65536) {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<MX, TWO, SP>),
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_kernel<MX, TWO, NT, SP>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
     if (attr != hipSuccess) return attr;
   }
-  hipLaunchKernelGGL((matvec_kernel<MX, TWO, SP>), dim3(slices * (nb + (rp > 0 ? 1 : 0))), dim3(MV_THREADS), lds, st, X, ldx, inv,
-                     l1t, wv, M, N, K, rp, nb, part, tpart);
+  hipLaunchKernelGGL((matvec_kernel<MX, TWO, NT, SP>), dim3(tb + slices * nb), dim3(MV_THREADS), lds, st, a.X, a.ldx, a.inv, a.l1t,
+                     a.wv, a.M, a.N, a.K, a.rp, nb, tb, a.part, a.tpart);
   return hipGetLastError();
 }
 
-template <bool MX, bool TWO>
-hipError_t dispatch(int sp, const uint16_t* X, int ldx, const float* inv, const uint16_t* l1t, const uint8_t* wv, int M, int N,
-                    int K, int rp, float* part, float* tpart, hipStream_t st) {
+template <bool MX, bool TWO, int NT>
+hipError_t dispatch(int sp, const MatvecArgs& a, hipStream_t st) {
   switch (sp) {
-    case 8: return launch<MX, TWO, 8>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
-    case 4: return launch<MX, TWO, 4>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
-    case 2: return launch<MX, TWO, 2>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
-    default: return launch<MX, TWO, 1>(X, ldx, inv, l1t, wv, M, N, K, rp, part, tpart, st);
+    case 8: return launch<MX, TWO, NT, 8>(a, st);
+    case 4: return launch<MX, TWO, NT, 4>(a, st);
+    case 2: return launch<MX, TWO, NT, 2>(a, st);
+    default: return launch<MX, TWO, NT, 1>(a, st);
   }
+}
+
+template <bool MX>
+hipError_t dispatch(int sp, const MatvecArgs& a, hipStream_t st) {
+  if (a.M <= 8) return dispatch<MX, false, 1>(sp, a, st);
+  return mv_nt(a.M, a.N) == 2 ? dispatch<MX, true, 2>(sp, a, st) : dispatch<MX, true, 1>(sp, a, st);
 }
 
 w4a4_status_t check_matvec(int M, int N, int K, int rank, int fmt) {
@@ -328,9 +396,9 @@ w4a4_status_t w4a4_matvec_sizes(int M, int N, int K, int rank, int fmt, size_t* 
   const w4a4_status_t s = check_matvec(M, N, K, rank, fmt);
   if (s != W4A4_OK) return s;
   if (!wv || !ws) return W4A4_ERR_INVALID_ARG;
-  const size_t P = mv_pairs(K), tiles = mv_tiles(N), sp = mv_slice(N, K), slices = (P + sp - 1) / sp;
+  const size_t P = mv_pairs(K), tiles = mv_tiles(N), sp = mv_slice(M, N, K), slices = (P + sp - 1) / sp;
   *wv = tiles * P * (1024 + 64);
-  *ws = slices * M * (tiles * 16 + rank_pad_of(rank)) * sizeof(float);
+  *ws = M * (slices * tiles * 16 + (size_t)mv_tslices(K) * rank_pad_of(rank)) * sizeof(float);
   return W4A4_OK;
 }
 
@@ -355,20 +423,15 @@ w4a4_status_t w4a4_matvec(const uint16_t* X, int M, int K, int ldx, const float*
   if (!aligned16(X) || !aligned16(inv_lambda) || !aligned16(wv) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(Y) & 1u) ||
       (rank > 0 && (!aligned16(l1t) || !aligned16(l2t))) || (reinterpret_cast<uintptr_t>(bias) & 1u))
     return W4A4_ERR_INVALID_ARG;
-  const int rp = rank_pad_of(rank), sp = mv_slice(N, K), slices = (mv_pairs(K) + sp - 1) / sp;
+  const int rp = rank_pad_of(rank), sp = mv_slice(M, N, K), slices = (mv_pairs(K) + sp - 1) / sp;
   float* part = static_cast<float*>(ws);
   float* tpart = part + (size_t)slices * M * (mv_tiles(N) * 16);
+  const MatvecArgs a{X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart};
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const bool mx = fmt == W4A4_FMT_MXFP4_B32;
-  hipError_t e;
-  if (M <= 8)
-    e = mx ? dispatch<true, false>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st)
-           : dispatch<false, false>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st);
-  else
-    e = mx ? dispatch<true, true>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st)
-           : dispatch<false, true>(sp, X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart, st);
+  const hipError_t e = fmt == W4A4_FMT_MXFP4_B32 ? dispatch<true>(sp, a, st) : dispatch<false>(sp, a, st);
   if (e != hipSuccess) return W4A4_ERR_HIP;
-  hipLaunchKernelGGL(matvec_finish_kernel, dim3((N + 63) / 64), dim3(256), 0, st, part, tpart, slices, l2t, bias, M, N, rp, Y, ldy);
+  hipLaunchKernelGGL(matvec_finish_kernel, dim3((N + 127) / 128, M), dim3(256), 0, st, part, slices, tpart, mv_tslices(K), l2t, bias, M,
+                     N, rp, Y, ldy);
   return hipGetLastError() == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
 }
 

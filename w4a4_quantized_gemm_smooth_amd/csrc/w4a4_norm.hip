@@ -346,8 +346,10 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
   __shared__ float red[16][65];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
   float s = 0.f;
-  if (k < 2 * K)
+  if (k < 2 * K) {
+#pragma unroll 16
     for (int r = w; r < rows; r += 16) s += part[(size_t)r * 2 * K + k];
+  }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && k < 2 * K) {
