@@ -62,15 +62,31 @@ struct __attribute__((aligned(16))) Slot {
   uint8_t b[TB * KSTEP * 2];
 };
 
-__device__ __forceinline__ void act_of(int act, float g, float& a, float& slope) {
-  if (act == W4A4_ACT_SILU) {
-    const float p = 1.0f / (1.0f + __expf(-g));
+// act(g) and act'(g), without branches. GELU: Phi(-|g|) = (t/2) exp(P(t) - g^2/2), t = 1/(1 + |g|/(2 sqrt 2)),
+// where P interpolates ln(erfcx(x)/t), x = |g|/sqrt 2 = 2(1/t - 1), at the Chebyshev nodes of t in [0, 1]:
+// 2.5e-7 of the value, in the far tail too.
+template <int ACT>
+__device__ __forceinline__ void act_of(float g, float& a, float& slope) {
+  if constexpr (ACT == W4A4_ACT_SILU) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
     a = g * p;
     slope = p * (1.0f + g * (1.0f - p));
   } else {
-    const float p = 0.5f * (1.0f + erff(g * 0.70710678f));
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.35355339f, 1.0f)), e = -0.5f * g * g;
+    float q = 0.004769651219248772f;
+    q = fmaf(q, t, 0.14636138081550598f);
+    q = fmaf(q, t, -0.7684580683708191f);
+    q = fmaf(q, t, 1.4231719970703125f);
+    q = fmaf(q, t, -1.0869556665420532f);
+    q = fmaf(q, t, 0.2567150592803955f);
+    q = fmaf(q, t, -0.18006151914596558f);
+    q = fmaf(q, t, 0.09577241539955139f);
+    q = fmaf(q, t, 0.3741760849952698f);
+    q = fmaf(q, t, 1.000020980834961f);
+    q = fmaf(q, t, -1.265512228012085f);
+    const float tail = 0.5f * t * __expf(e + q), p = g < 0.f ? tail : 1.0f - tail;
     a = g * p;
-    slope = p + g * __expf(-0.5f * g * g) * 0.39894228f;
+    slope = fmaf(g * 0.39894228f, __expf(e), p);
   }
 }
 
@@ -103,6 +119,18 @@ __device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stag
       if (row < rows && col < cols) *reinterpret_cast<uint4*>(out + (size_t)row * ld + col) = val;
     }
   }
+}
+
+// The other way: 64 rows of one 32-column tile of a bf16 matrix -> stage (rows of 80 bytes), zeros outside.
+__device__ __forceinline__ void load_rows(const uint16_t* in, int ld, uint8_t* stage, int rows, int cols, int r0, int c0, int lane) {
+  uint4 v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = r0 + 16 * q + (lane >> 2), col = c0 + 8 * (lane & 3);
+    v[q] = row < rows && col < cols ? *reinterpret_cast<const uint4*>(in + (size_t)row * ld + col) : uint4{0u, 0u, 0u, 0u};
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + (16 * q + (lane >> 2)) * 80 + 16 * (lane & 3)) = v[q];
 }
 
 template <int AM, int BM, int EPI>
@@ -153,63 +181,62 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       vb[q] = row * 32 + 16 * ((lane & 1) ^ ((row >> 3) & 1)) | (n0 + row < g.cols ? 0 : OOB);
     }
   }
-  const int vs = 64 * dw + 4 * (lane & 15);   // CODES: this DMA wave's 64 scales
-  auto clamp31 = [](long long v) { return (int)(v < 0x7FFFFFFFLL ? v : 0x7FFFFFFFLL); };
-  auto rows_rsrc = [&](const void* p, int ld, int r0, int rows, int k0) {   // rows r0.., contraction from k0
-    const uint16_t* q = static_cast<const uint16_t*>(p) + (size_t)r0 * ld + k0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(q), 0, clamp31(((long long)(rows - r0 - 1) * ld + g.K - k0) * 2), RSRC_W3);
+  const int vs = (64 * dw + 4 * (lane & 15)) | (n0 + 64 * dw + 4 * (lane & 15) < g.cols ? 0 : OOB);   // CODES: this wave's 64 scales
+  // every offset outside an operand carries OOB, so the descriptors need no range of their own
+  auto rsrc = [](const void* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7FFFFFFF, RSRC_W3); };
+  const int krow = lane >> 5;   // COLS: which of an instruction's two contraction rows
+  // Copies of step i of this block's (past the end: zeros) into a slot. ROWS: the step moves the scalar
+  // offset (a row is below 2^22 bytes); COLS: the 64-bit base.
+  auto step_of = [&](int i, int& past, int& seg, int& k0) {
+    const int s = s_lo + min(i, S - 1);
+    past = i < S ? 0 : OOB;
+    seg = s >= g.steps ? 1 : 0;
+    k0 = (s - seg * g.steps) * KSTEP;
   };
-  auto cols_rsrc = [&](const void* p, int ld, int c0, int cols, int k0) {   // contraction rows k0.., columns c0..
-    const uint16_t* q = static_cast<const uint16_t*>(p) + (size_t)k0 * ld + c0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(q), 0, clamp31(((long long)(g.K - k0 - 1) * ld + cols - c0) * 2), RSRC_W3);
-  };
-  auto dma = [&](int i, Slot* sl) {   // step i of this block's; past the end: zeros
-    const int past = i < S ? 0 : OOB, s = s_lo + min(i, S - 1), seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
-    const void* pa = g.A[prob + seg];
-    if constexpr (AM == ROWS) {
-      const __amdgpu_buffer_rsrc_t r = rows_rsrc(pa, g.lda, m0, g.rows, k0);
-      const int o = past | (k0 + ka < g.K ? 0 : OOB);
+  auto copy = [&](uint8_t* dst, int mode, const void* p, int ld, int first, int k0, int past, const int (&v)[4], int koff) {
+    if (mode == ROWS) {
+      const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint16_t*>(p) + (size_t)first * ld);
+      const int o = past | (k0 + koff < g.K ? 0 : OOB);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * dw + q)), 16, va[q] | o, 0, 0, 0);
+      for (int q = 0; q < 4; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + 1024 * (4 * dw + q)), 16, v[q] | o, k0 * 2, 0, 0);
     } else {
-      const __amdgpu_buffer_rsrc_t r = cols_rsrc(pa, g.lda, m0, g.rows, k0);
+      const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint16_t*>(p) + (size_t)k0 * ld + first);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int o = past | (k0 + 2 * (4 * dw + q) + (lane >> 5) < g.K ? 0 : OOB);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * dw + q)), 16, va[q] | o, 0, 0, 0);
+        const int o = past | (k0 + 2 * (4 * dw + q) + krow < g.K ? 0 : OOB);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + 1024 * (4 * dw + q)), 16, v[q] | o, 0, 0, 0);
       }
     }
+  };
+  auto dma_a = [&](int i, Slot* sl) {
+    int past, seg, k0;
+    step_of(i, past, seg, k0);
+    copy(sl->a, AM, g.A[prob + seg], g.lda, m0, k0, past, va, ka);
+  };
+  auto dma_b = [&](int i, Slot* sl) {
+    int past, seg, k0;
+    step_of(i, past, seg, k0);
     if constexpr (GATED) {
-      const __amdgpu_buffer_rsrc_t r0 = rows_rsrc(g.B[0], g.ldb, n0, g.cols, k0), r1 = rows_rsrc(g.B[1], g.ldb, n0, g.cols, k0);
+      const __amdgpu_buffer_rsrc_t r0 = rsrc(static_cast<const uint16_t*>(g.B[0]) + (size_t)n0 * g.ldb),
+                                   r1 = rsrc(static_cast<const uint16_t*>(g.B[1]) + (size_t)n0 * g.ldb);
       const int o = past | (k0 + kb < g.K ? 0 : OOB);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
-    } else if constexpr (BM == ROWS) {
-      const __amdgpu_buffer_rsrc_t r = rows_rsrc(g.B[seg], g.ldb, n0, g.cols, k0);
-      const int o = past | (k0 + kb < g.K ? 0 : OOB);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
-    } else if constexpr (BM == COLS) {
-      const __amdgpu_buffer_rsrc_t r = cols_rsrc(g.B[seg], g.ldb, n0, g.cols, k0);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int o = past | (k0 + 2 * (4 * dw + q) + (lane >> 5) < g.K ? 0 : OOB);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, 0, 0, 0);
-      }
-    } else {
-      const size_t c = (size_t)s * g.cols + n0;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(static_cast<const uint8_t*>(g.B[0]) + c * 32), 0, clamp31((long long)(g.cols - n0) * 32), RSRC_W3);
-      const __amdgpu_buffer_rsrc_t rs =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.scales + c), 0, g.cols - n0, RSRC_W3);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, k0 * 2, 0, 0);
+    } else if constexpr (BM == CODES) {
+      const size_t c = (size_t)(s_lo + min(i, S - 1)) * g.cols + n0;
+      const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint8_t*>(g.B[0]) + c * 32), rs = rsrc(g.scales + c);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (2 * dw + q)), 16, vb[q] | past, 0, 0, 0);
       if (lane < 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(sl->b + 8192 + 64 * dw), 4, vs | past, 0, 0, 0);
+    } else {
+      copy(sl->b, BM, g.B[seg], g.ldb, n0, k0, past, vb, kb);
     }
+  };
+  auto dma = [&](int i, Slot* sl) {
+    dma_a(i, sl);
+    dma_b(i, sl);
   };
 
   // ---- operands of sub-step s (16 of the contraction) of a slot
@@ -275,6 +302,27 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   rd(ring[0], 0, A[0], B[0]);
+  auto mfmas = [&](const v4i (&a)[4], const v4i (&b)[2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a[i]), as_bf16x8(b[j]), acc[i][j], 0, 0, 0);
+  };
+  // half a step's order: the next half's operands are read between this half's first matrix instructions
+  auto order = [](auto copies) {
+    constexpr int NRD = (AM == COLS ? 8 : 4) + (BM == COLS ? 4 : BM == ROWS ? 2 : 4), PER = (NRD + 5) / 6;
+#pragma unroll
+    for (int q = 0; q < 6; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // one MFMA
+      __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);   // LDS reads
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);   // copies
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, copies.value - 2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto main_loop = [&](auto tag) {
     constexpr bool D = decltype(tag)::value;
     for (int i0 = 0; i0 < S; i0 += NSLOT) {
@@ -285,19 +333,13 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
         asm volatile("" ::: "memory");   // the other waves' copies change the slots: no read moves over it
         __builtin_amdgcn_sched_barrier(0);
         rd(ring[u], 1, A[1], B[1]);
-        if (D) dma(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(A[0][i]), as_bf16x8(B[0][j]), acc[i][j], 0, 0, 0);
+        if (D) dma_a(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
+        mfmas(A[0], B[0]);
+        order(std::integral_constant<int, D ? 4 : 0>{});
         rd(ring[(u + 1) % NSLOT], 0, A[0], B[0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(A[1][i]), as_bf16x8(B[1][j]), acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        if (D) dma_b(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
+        mfmas(A[1], B[1]);
+        order(std::integral_constant<int, D ? NDMA - 4 : 0>{});
       }
     }
   };
@@ -331,22 +373,32 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
         }
       }
   } else {
-    const int c0 = n0 + 32 * wn, col = c0 + lr;
+    const int c0 = n0 + 32 * wn;
+    if constexpr (EPI == OUT_GATED_GRAD) {   // dH's rows: 2 x 64 of them, 5 KB each
+      load_rows(g.dH, g.lddh, stage, g.rows, g.cols, r0, c0, lane);
+      load_rows(g.dH, g.lddh, stage + 64 * 80, g.rows, g.cols, r0 + 64, c0, lane);
+    }
+    auto apply = [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        float a, slope;
-        act_of(g.act, acc[i][0][v], a, slope);
-        if constexpr (EPI == OUT_GATED) {
-          acc[i][0][v] = a * acc[i][1][v];
-        } else {
-          const int row = r0 + 32 * i + 8 * (v >> 2) + 4 * lh + (v & 3);
-          const float dh = row < g.rows && col < g.cols ? bf16f(g.dH[(size_t)row * g.lddh + col]) : 0.f;
-          acc[i][0][v] = dh * acc[i][1][v] * slope;
-          acc[i][1][v] = dh * a;
+        for (int v = 0; v < 16; ++v) {
+          float a, slope;
+          act_of<act.value>(acc[i][0][v], a, slope);
+          if constexpr (EPI == OUT_GATED) {
+            acc[i][0][v] = a * acc[i][1][v];
+          } else {
+            const float dh = bf16f(*reinterpret_cast<const uint16_t*>(stage + (32 * i + 8 * (v >> 2) + 4 * lh + (v & 3)) * 80 + 2 * lr));
+            acc[i][0][v] = dh * acc[i][1][v] * slope;
+            acc[i][1][v] = dh * a;
+          }
+          if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // a few values' temporaries at a time
         }
-      }
+    };
+    if (g.act == W4A4_ACT_SILU)
+      apply(std::integral_constant<int, W4A4_ACT_SILU>{});
+    else
+      apply(std::integral_constant<int, W4A4_ACT_GELU>{});
     store_block<0, 1>(acc, stage, static_cast<uint16_t*>(g.out[0]), g.ldo, g.rows, g.cols, r0, c0, lane);
     if constexpr (EPI == OUT_GATED_GRAD)
       store_block<1, 1>(acc, stage, static_cast<uint16_t*>(g.out[1]), g.ldo, g.rows, g.cols, r0, c0, lane);
@@ -414,7 +466,10 @@ __global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16
     us += red[w][1][m][c];
   }
   float a, slope;
-  act_of(act, gs, a, slope);
+  if (act == W4A4_ACT_SILU)
+    act_of<W4A4_ACT_SILU>(gs, a, slope);
+  else
+    act_of<W4A4_ACT_GELU>(gs, a, slope);
   H[(size_t)m * ldh + col] = (uint16_t)pack_bf16x2(a * us, 0.f);
 }
 
