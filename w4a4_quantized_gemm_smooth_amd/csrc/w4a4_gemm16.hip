@@ -55,7 +55,9 @@ struct GemmArgs {
   int act;
 };
 
-__device__ __forceinline__ int cols_sw(int k, bool perm) { return 2 * ((k & 3) | (((perm ? k >> 4 : k >> 3) & 1) << 2)); }
+// COLS: the four rows that a transposing read takes for 16 lanes, and the two column halves beside them,
+// lie in the eight different 32-byte parts of 256 bytes
+__device__ __forceinline__ int cols_sw(int k) { return 4 * (k & 3); }
 
 struct __attribute__((aligned(16))) Slot {
   uint8_t a[TB * KSTEP * 2];
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       const int row = 64 * dw + 16 * q + (lane >> 2);
       va[q] = (row * g.lda + ka) * 2 | (m0 + row < g.rows ? 0 : OOB);
     } else {
-      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk, PERM);
+      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk);
       va[q] = (kk * g.lda + 8 * c) * 2 | (m0 + 8 * c < g.rows ? 0 : OOB);
     }
     if constexpr (GATED) {
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       const int row = 64 * dw + 16 * q + (lane >> 2);
       vb[q] = (row * g.ldb + kb) * 2 | (n0 + row < g.cols ? 0 : OOB);
     } else if constexpr (BM == COLS) {
-      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk, PERM);
+      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk);
       vb[q] = (kk * g.ldb + 8 * c) * 2 | (n0 + 8 * c < g.cols ? 0 : OOB);
     } else {
       const int row = 64 * dw + 32 * (q & 1) + (lane >> 1);
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   int ra[4], rb[4];   // LDS offsets: ROWS [s]; COLS [tile]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int i16 = lane & 15, mh = (lane >> 4) & 1, kk = (PERM ? 16 : 8) * lh + (i16 >> 2), sw = cols_sw(kk, PERM);
+    const int i16 = lane & 15, mh = (lane >> 4) & 1, kk = (PERM ? 16 : 8) * lh + (i16 >> 2), sw = cols_sw(kk);
     if (AM == ROWS)
       ra[i] = (128 * wm + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
     else
@@ -257,6 +259,8 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   }
   auto tr = [](const uint8_t* p) { return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)p)); };
   auto two = [](v2i x, v2i y) { return v4i{x[0], x[1], y[0], y[1]}; };
+  v4i code[2];      // CODES: a lane's 16 codes of a step, both sub-steps', read with the first
+  float scale[2];   // 2^e from its byte: 0 is the subnormal 2^-127; 255 gives Inf, and NaN with its codes of 0
   auto rd = [&](Slot* sl, int s, v4i (&A)[4], v4i (&B)[2]) {
     constexpr int SUB = (PERM ? 8 : 16) * 512;   // bytes from sub-step 0 to 1 in a COLS slot
 #pragma unroll
@@ -273,13 +277,16 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       } else if constexpr (BM == COLS) {
         B[j] = two(tr(sl->b + rb[j] + SUB * s), tr(sl->b + rb[j] + SUB * s + 4 * 512));
       } else {
-        const v2i c = *reinterpret_cast<const v2i*>(sl->b + rb[j] + 8 * s);
-        const uint32_t e = sl->b[8192 + 64 * wn + 32 * j + lr];
-        const float sc = e == 255u ? __uint_as_float(0x7FC00000u) : e == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
+        if (s == 0) {
+          code[j] = *reinterpret_cast<const v4i*>(sl->b + rb[j]);
+          const uint32_t e = sl->b[8192 + 64 * wn + 32 * j + lr];
+          scale[j] = __uint_as_float(max(e << 23, 0x00400000u));
+        }
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const int w = c[d >> 1] >> (16 * (d & 1));
-          B[j][d] = (int)pack_bf16x2((float)(int8_t)w * sc, (float)(int8_t)(w >> 8) * sc);
+          const uint32_t w = (uint32_t)code[j][2 * s + (d >> 1)];
+          const int8_t q0 = (int8_t)(d & 1 ? w >> 16 : w), q1 = (int8_t)(d & 1 ? w >> 24 : w >> 8);
+          B[j][d] = (int)pack_bf16x2((float)q0 * scale[j], (float)q1 * scale[j]);
         }
       }
     }
