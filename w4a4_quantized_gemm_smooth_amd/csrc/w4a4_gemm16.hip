@@ -8,9 +8,11 @@
 // kernel of its own.
 //
 // The product kernel. Blocks of 256 x 256 outputs, eight waves of 128 x 64 (4 x 2 tiles of 32x32, 128
-// accumulators to a lane). A step is 32 of the contraction: 16 KB an operand in one of four ring slots
-// in LDS, copied global -> LDS three steps ahead by the LDS DMA path of waves 0..3. Operands are copied
-// as they lie in memory, whichever of their axes is contiguous:
+// accumulators to a lane). A step is 32 of the contraction: 16 KB an operand in one of four ring slots in
+// LDS, copied global -> LDS by the LDS DMA path of waves 0..3 (one a SIMD, so that an issue that stalls
+// holds up one of the SIMD's two waves) three steps ahead; the operands of half a step (16 of the
+// contraction) are read between the matrix instructions of the half before. Operands are copied as they
+// lie in memory, whichever of their axes is contiguous:
 //   ROWS   contraction contiguous: LDS row = output row, 64 bytes of contraction; a lane's operand (8 of
 //          the contraction) is one 16-byte read. Chunk c of row r is kept at c ^ ((r >> 2) & 3).
 //   COLS   output axis contiguous: LDS row = one of the contraction, 512 bytes of the output axis; a
@@ -19,7 +21,8 @@
 //   CODES  8-bit codes with a scale per column and step (B only): 32 bytes of contraction to a column,
 //          converted after the read; the values are bf16 numbers, so nothing is rounded.
 // Outside its range a copy's address is moved past the buffer's end, which reads as zero, so ragged
-// sizes cost nothing in the loop.
+// sizes cost nothing in the loop. bf16 results are computed transposed (B as the first operand), which
+// leaves a lane four neighbouring columns of a row.
 #include <type_traits>
 
 #include "w4a4_device_common.h"
@@ -32,7 +35,7 @@ namespace {
 enum : int { ROWS = 0, COLS = 1, CODES = 2 };
 enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_GATED = 2, OUT_GATED_GRAD = 3 };
 
-constexpr int TB = 256;          // block rows and columns
+constexpr int TM = 256, TN = 256;   // block rows and columns
 constexpr int KSTEP = 32;        // contraction per step
 constexpr int NSLOT = 4;         // ring slots
 constexpr int GM_THREADS = 512;
@@ -52,7 +55,6 @@ struct GemmArgs {
   int rows, cols, K;               // per problem; K per segment; gated: cols of one weight
   int segs, probs, steps;          // steps per segment
   int splits;                      // parts of the contraction, each to its own plane of out[0] (OUT_F32)
-  int act;
 };
 
 // COLS: the four rows that a transposing read takes for 16 lanes, and the two column halves beside them,
@@ -60,8 +62,8 @@ struct GemmArgs {
 __device__ __forceinline__ int cols_sw(int k) { return 4 * (k & 3); }
 
 struct __attribute__((aligned(16))) Slot {
-  uint8_t a[TB * KSTEP * 2];
-  uint8_t b[TB * KSTEP * 2];
+  uint8_t a[TM * KSTEP * 2];
+  uint8_t b[TN * KSTEP * 2];
 };
 
 // act(g) and act'(g), without branches. GELU: Phi(-|g|) = (t/2) exp(P(t) - g^2/2), t = 1/(1 + |g|/(2 sqrt 2)),
@@ -92,8 +94,9 @@ __device__ __forceinline__ void act_of(float g, float& a, float& slope) {
   }
 }
 
-// The wave's 32-column tiles J0 .. J0 + NT - 1, fp32 -> bf16 through LDS, in whole 16-byte pieces of rows.
-// `stage`: 64 rows of NT * 64 + 16 bytes. cols is a multiple of 8, rows are 16-byte aligned.
+// The wave's 32-column tiles J0 .. J0 + NT - 1 of transposed results (a lane: row lane % 32 of each 32-row
+// tile, columns 8 (v / 4) + 4 (lane / 32) + v % 4), fp32 -> bf16 through LDS, in whole 16-byte pieces of
+// rows. `stage`: 64 rows of NT * 64 + 16 bytes. cols is a multiple of 8, rows are 16-byte aligned.
 template <int J0, int NT>
 __device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stage, uint16_t* out, int ld, int rows, int cols,
                                             int r0, int c0, int lane) {
@@ -106,12 +109,10 @@ __device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stag
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; v += 2) {
-          const int rl = ii * 32 + 8 * (v >> 2) + 4 * lh + (v & 3);
-          const uint32_t pr = pack_bf16x2(t[2 * half + ii][J0 + j][v], t[2 * half + ii][J0 + j][v + 1]);
-          uint16_t* d = reinterpret_cast<uint16_t*>(stage + rl * ES + (j * 32 + lr) * 2);
-          d[0] = (uint16_t)pr;
-          d[ES / 2] = (uint16_t)(pr >> 16);
+        for (int v = 0; v < 16; v += 4) {
+          const v16f& x = t[2 * half + ii][J0 + j];
+          *reinterpret_cast<uint2*>(stage + (ii * 32 + lr) * ES + j * 64 + 4 * v + 8 * lh) =
+              uint2{pack_bf16x2(x[v], x[v + 1]), pack_bf16x2(x[v + 2], x[v + 3])};
         }
 #pragma unroll
     for (int q = 0; q < CPR; ++q) {
@@ -135,11 +136,12 @@ __device__ __forceinline__ void load_rows(const uint16_t* in, int ld, uint8_t* s
   for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + (16 * q + (lane >> 2)) * 80 + 16 * (lane & 3)) = v[q];
 }
 
-template <int AM, int BM, int EPI>
+template <int AM, int BM, int EPI, int ACT = 0>
 __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g) {
   constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
   constexpr bool PERM = BM == CODES;   // contraction order of a step: 16 h + 8 s + e instead of 16 s + 8 h + e
-  constexpr int NDMA = 4 + (BM == CODES ? 3 : 4);
+  constexpr bool SWAP = EPI != OUT_F32;
+  constexpr int NA = 4, NB = BM == CODES ? 3 : 4, NDMA = NA + NB;   // copies per copying wave and step
   static_assert(!GATED || (AM == ROWS && BM == ROWS), "gated: both operands by rows");
   __shared__ Slot sl0, sl1, sl2, sl3;
   Slot* const ring[NSLOT] = {&sl0, &sl1, &sl2, &sl3};
@@ -147,95 +149,99 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3, dw = wave & 3;
-  const int tiles_n = (g.cols + (GATED ? TB / 2 : TB) - 1) / (GATED ? TB / 2 : TB), tiles_mp = (g.rows + TB - 1) / TB;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
+  const int tiles_n = (g.cols + (GATED ? TN / 2 : TN) - 1) / (GATED ? TN / 2 : TN), tiles_mp = (g.rows + TM - 1) / TM;
   int tm, tn;
   tile_of(blockIdx.x, gridDim.x, tiles_mp * g.probs, tiles_n, tm, tn);
-  const int prob = tm / tiles_mp, m0 = (tm % tiles_mp) * TB, n0 = tn * (GATED ? TB / 2 : TB);
+  const int prob = tm / tiles_mp, m0 = (tm % tiles_mp) * TM, n0 = tn * (GATED ? TN / 2 : TN);
   const int all = g.steps * g.segs, s_lo = (int)((long long)all * blockIdx.y / g.splits),
             s_hi = (int)((long long)all * (blockIdx.y + 1) / g.splits), S = s_hi - s_lo;
 
-  // ---- copies: instruction q of DMA wave dw, the lane's source offset (with OOB) and contraction index
-  int va[4], vb[4];
-  int ka, kb;   // ROWS: the chunk's contraction offset in a step
-  ka = 8 * ((lane & 3) ^ ((lane >> 4) & 3));
-  kb = ka;
+  // ---- copies: instruction q of copying wave wn fills the KB 4 wn + q of an operand; the lane's source
+  // offset (with OOB), and its contraction index in the step
+  int va[NA], vb[4];
+  const int kc = 8 * ((lane & 3) ^ ((lane >> 4) & 3));   // ROWS: 16 rows an instruction, this lane's chunk
+  const int ra4 = lane >> 2;
+  auto krow = [&](int t) { return 2 * t + (lane >> 5); };   // COLS: two rows an instruction
+  auto kcol = [&](int t) { return 8 * ((lane & 31) ^ cols_sw(krow(t))); };
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    const int t = 4 * wn + q;
+    if constexpr (AM == ROWS)
+      va[q] = ((16 * t + ra4) * g.lda + kc) * 2 | (m0 + 16 * t + ra4 < g.rows ? 0 : OOB);
+    else
+      va[q] = (krow(t) * g.lda + kcol(t)) * 2 | (m0 + kcol(t) < g.rows ? 0 : OOB);
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if constexpr (AM == ROWS) {
-      const int row = 64 * dw + 16 * q + (lane >> 2);
-      va[q] = (row * g.lda + ka) * 2 | (m0 + row < g.rows ? 0 : OOB);
-    } else {
-      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk);
-      va[q] = (kk * g.lda + 8 * c) * 2 | (m0 + 8 * c < g.rows ? 0 : OOB);
-    }
-    if constexpr (GATED) {
-      const int row = 32 * dw + 16 * (q & 1) + (lane >> 2);
-      vb[q] = (row * g.ldb + kb) * 2 | (n0 + row < g.cols ? 0 : OOB);
+    const int t = 4 * wn + q;
+    if constexpr (GATED) {   // a wave's 64 rows: 32 of the one weight, 32 of the other
+      const int row = 32 * wn + 16 * (q & 1) + ra4;
+      vb[q] = (row * g.ldb + kc) * 2 | (n0 + row < g.cols ? 0 : OOB);
     } else if constexpr (BM == ROWS) {
-      const int row = 64 * dw + 16 * q + (lane >> 2);
-      vb[q] = (row * g.ldb + kb) * 2 | (n0 + row < g.cols ? 0 : OOB);
+      vb[q] = ((16 * t + ra4) * g.ldb + kc) * 2 | (n0 + 16 * t + ra4 < g.cols ? 0 : OOB);
     } else if constexpr (BM == COLS) {
-      const int kk = 2 * (4 * dw + q) + (lane >> 5), c = (lane & 31) ^ cols_sw(kk);
-      vb[q] = (kk * g.ldb + 8 * c) * 2 | (n0 + 8 * c < g.cols ? 0 : OOB);
+      vb[q] = (krow(t) * g.ldb + kcol(t)) * 2 | (n0 + kcol(t) < g.cols ? 0 : OOB);
     } else {
-      const int row = 64 * dw + 32 * (q & 1) + (lane >> 1);
-      vb[q] = row * 32 + 16 * ((lane & 1) ^ ((row >> 3) & 1)) | (n0 + row < g.cols ? 0 : OOB);
+      const int row = 64 * wn + 32 * (q & 1) + (lane >> 1);
+      vb[q] = (row * 32 + 16 * ((lane & 1) ^ ((row >> 3) & 1))) | (n0 + row < g.cols ? 0 : OOB);
     }
   }
-  const int vs = (64 * dw + 4 * (lane & 15)) | (n0 + 64 * dw + 4 * (lane & 15) < g.cols ? 0 : OOB);   // CODES: this wave's 64 scales
+  const int vs = (64 * wn + 4 * (lane & 15)) | (n0 + 64 * wn + 4 * (lane & 15) < g.cols ? 0 : OOB);   // CODES: 64 scales
   // every offset outside an operand carries OOB, so the descriptors need no range of their own
   auto rsrc = [](const void* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7FFFFFFF, RSRC_W3); };
-  const int krow = lane >> 5;   // COLS: which of an instruction's two contraction rows
-  // Copies of step i of this block's (past the end: zeros) into a slot. ROWS: the step moves the scalar
-  // offset (a row is below 2^22 bytes); COLS: the 64-bit base.
-  auto step_of = [&](int i, int& past, int& seg, int& k0) {
-    const int s = s_lo + min(i, S - 1);
-    past = i < S ? 0 : OOB;
-    seg = s >= g.steps ? 1 : 0;
-    k0 = (s - seg * g.steps) * KSTEP;
-  };
-  auto copy = [&](uint8_t* dst, int mode, const void* p, int ld, int first, int k0, int past, const int (&v)[4], int koff) {
-    if (mode == ROWS) {
-      const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint16_t*>(p) + (size_t)first * ld);
-      const int o = past | (k0 + koff < g.K ? 0 : OOB);
+  // ROWS: a step moves the scalar offset (a row is below 2^22 bytes); COLS: the 64-bit base.
+  auto rows_at = [&](const void* p, int ld, int first) { return rsrc(static_cast<const uint16_t*>(p) + (size_t)first * ld); };
+  auto cols_at = [&](const void* p, int ld, int first, int k0) { return rsrc(static_cast<const uint16_t*>(p) + (size_t)k0 * ld + first); };
+  auto dma_a = [&](int i, Slot* sl) {   // step i of this block's; past the end: zeros
+    const int s = s_lo + min(i, S - 1), past = i < S ? 0 : OOB, seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
+    const int kin = past | (k0 + kc < g.K ? 0 : OOB);
+    auto in = [&](int t) { return past | (k0 + krow(t) < g.K ? 0 : OOB); };
+    if constexpr (AM == ROWS) {
+      const __amdgpu_buffer_rsrc_t r = rows_at(g.A[prob + seg], g.lda, m0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + 1024 * (4 * dw + q)), 16, v[q] | o, k0 * 2, 0, 0);
+      for (int q = 0; q < NA; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * wn + q)), 16, va[q] | kin, k0 * 2, 0, 0);
     } else {
-      const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint16_t*>(p) + (size_t)k0 * ld + first);
+      const __amdgpu_buffer_rsrc_t r = cols_at(g.A[prob + seg], g.lda, m0, k0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int o = past | (k0 + 2 * (4 * dw + q) + krow < g.K ? 0 : OOB);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(dst + 1024 * (4 * dw + q)), 16, v[q] | o, 0, 0, 0);
+      for (int q = 0; q < NA; ++q) {   // (no call in the builtin's arguments: the host pass would lose the kernel's stub)
+        const int v = va[q] | in(4 * wn + q);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * wn + q)), 16, v, 0, 0, 0);
       }
     }
   };
-  auto dma_a = [&](int i, Slot* sl) {
-    int past, seg, k0;
-    step_of(i, past, seg, k0);
-    copy(sl->a, AM, g.A[prob + seg], g.lda, m0, k0, past, va, ka);
-  };
   auto dma_b = [&](int i, Slot* sl) {
-    int past, seg, k0;
-    step_of(i, past, seg, k0);
+    const int s = s_lo + min(i, S - 1), past = i < S ? 0 : OOB, seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
+    const int kin = past | (k0 + kc < g.K ? 0 : OOB);
+    auto in = [&](int t) { return past | (k0 + krow(t) < g.K ? 0 : OOB); };
     if constexpr (GATED) {
-      const __amdgpu_buffer_rsrc_t r0 = rsrc(static_cast<const uint16_t*>(g.B[0]) + (size_t)n0 * g.ldb),
-                                   r1 = rsrc(static_cast<const uint16_t*>(g.B[1]) + (size_t)n0 * g.ldb);
-      const int o = past | (k0 + kb < g.K ? 0 : OOB);
+      const __amdgpu_buffer_rsrc_t r0 = rows_at(g.B[0], g.ldb, n0), r1 = rows_at(g.B[1], g.ldb, n0);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * dw + q)), 16, vb[q] | o, k0 * 2, 0, 0);
-    } else if constexpr (BM == CODES) {
-      const size_t c = (size_t)(s_lo + min(i, S - 1)) * g.cols + n0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, vb[q] | kin, k0 * 2, 0, 0);
+    } else if constexpr (BM == ROWS) {
+      const __amdgpu_buffer_rsrc_t r = rows_at(g.B[seg], g.ldb, n0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, vb[q] | kin, k0 * 2, 0, 0);
+    } else if constexpr (BM == COLS) {
+      const __amdgpu_buffer_rsrc_t r = cols_at(g.B[seg], g.ldb, n0, k0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int v = vb[q] | in(4 * wn + q);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, v, 0, 0, 0);
+      }
+    } else {
+      const size_t c = (size_t)s * g.cols + n0;
       const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint8_t*>(g.B[0]) + c * 32), rs = rsrc(g.scales + c);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (2 * dw + q)), 16, vb[q] | past, 0, 0, 0);
-      if (lane < 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(sl->b + 8192 + 64 * dw), 4, vs | past, 0, 0, 0);
-    } else {
-      copy(sl->b, BM, g.B[seg], g.ldb, n0, k0, past, vb, kb);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (2 * wn + q)), 16, vb[q] | past, 0, 0, 0);
+      if (lane < 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(sl->b + 8192 + 64 * wn), 4, vs | past, 0, 0, 0);
     }
   };
+
   auto dma = [&](int i, Slot* sl) {
     dma_a(i, sl);
     dma_b(i, sl);
@@ -262,20 +268,20 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   v4i code[2];      // CODES: a lane's 16 codes of a step, both sub-steps', read with the first
   float scale[2];   // 2^e from its byte: 0 is the subnormal 2^-127; 255 gives Inf, and NaN with its codes of 0
   auto rd = [&](Slot* sl, int s, v4i (&A)[4], v4i (&B)[2]) {
-    constexpr int SUB = (PERM ? 8 : 16) * 512;   // bytes from sub-step 0 to 1 in a COLS slot
+    constexpr int SUB = PERM ? 8 : 16;   // contraction rows from sub-step 0 to 1 in a COLS slot
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (AM == ROWS)
         A[i] = *reinterpret_cast<const v4i*>(sl->a + ra[s] + 2048 * i);
       else
-        A[i] = two(tr(sl->a + ra[i] + SUB * s), tr(sl->a + ra[i] + SUB * s + 4 * 512));
+        A[i] = two(tr(sl->a + ra[i] + SUB * 512 * s), tr(sl->a + ra[i] + SUB * 512 * s + 4 * 512));
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (BM == ROWS) {
         B[j] = *reinterpret_cast<const v4i*>(sl->b + rb[s] + 2048 * j);
       } else if constexpr (BM == COLS) {
-        B[j] = two(tr(sl->b + rb[j] + SUB * s), tr(sl->b + rb[j] + SUB * s + 4 * 512));
+        B[j] = two(tr(sl->b + rb[j] + SUB * 512 * s), tr(sl->b + rb[j] + SUB * 512 * s + 4 * 512));
       } else {
         if (s == 0) {
           code[j] = *reinterpret_cast<const v4i*>(sl->b + rb[j]);
@@ -299,22 +305,12 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  v4i A[2][4], B[2][2];
-  const bool dma_wave = wave < 4;
-  if (dma_wave) {
-#pragma unroll
-    for (int i = 0; i < NSLOT - 1; ++i) dma(i, ring[i]);
-    wait_vmcnt<NDMA * (NSLOT - 2)>();
-  }
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  rd(ring[0], 0, A[0], B[0]);
   auto mfmas = [&](const v4i (&a)[4], const v4i (&b)[2]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a[i]), as_bf16x8(b[j]), acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(SWAP ? b[j] : a[i]), as_bf16x8(SWAP ? a[i] : b[j]), acc[i][j], 0, 0, 0);
   };
   // half a step's order: the next half's operands are read between this half's first matrix instructions
   auto order = [](auto copies) {
@@ -330,6 +326,16 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
     if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, copies.value - 2, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
+  v4i A[2][4], B[2][2];
+  const bool copies = wave < 4;
+  if (copies) {
+#pragma unroll
+    for (int i = 0; i < NSLOT - 1; ++i) dma(i, ring[i]);
+    wait_vmcnt<NDMA * (NSLOT - 2)>();
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  rd(ring[0], 0, A[0], B[0]);
   auto main_loop = [&](auto tag) {
     constexpr bool D = decltype(tag)::value;
     for (int i0 = 0; i0 < S; i0 += NSLOT) {
@@ -342,15 +348,15 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
         rd(ring[u], 1, A[1], B[1]);
         if (D) dma_a(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
         mfmas(A[0], B[0]);
-        order(std::integral_constant<int, D ? 4 : 0>{});
+        order(std::integral_constant<int, D ? NA : 0>{});
         rd(ring[(u + 1) % NSLOT], 0, A[0], B[0]);
         if (D) dma_b(i0 + u + NSLOT - 1, ring[(u + NSLOT - 1) % NSLOT]);
         mfmas(A[1], B[1]);
-        order(std::integral_constant<int, D ? NDMA - 4 : 0>{});
+        order(std::integral_constant<int, D ? NB : 0>{});
       }
     }
   };
-  if (dma_wave)
+  if (copies)
     main_loop(std::true_type{});
   else
     main_loop(std::false_type{});
@@ -358,7 +364,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 
-  // ---- epilogue: lane holds column lr and rows 8 (v / 4) + 4 lh + v % 4 of each tile
+  // ---- epilogue
   uint8_t* stage = nullptr;
 #pragma unroll
   for (int w = 0; w < 8; ++w)
@@ -366,7 +372,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   const int r0 = m0 + 128 * wm;
   if constexpr (EPI == OUT_BF16) {
     store_block<0, 2>(acc, stage, static_cast<uint16_t*>(g.out[prob]), g.ldo, g.rows, g.cols, r0, n0 + 64 * wn, lane);
-  } else if constexpr (EPI == OUT_F32) {
+  } else if constexpr (EPI == OUT_F32) {   // lane: column lr, rows 8 (v / 4) + 4 lh + v % 4 of each tile
     float* out = static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -385,27 +391,27 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       load_rows(g.dH, g.lddh, stage, g.rows, g.cols, r0, c0, lane);
       load_rows(g.dH, g.lddh, stage + 64 * 80, g.rows, g.cols, r0 + 64, c0, lane);
     }
-    auto apply = [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
+      for (int v0 = 0; v0 < 16; v0 += 4) {
+        uint2 d = {0u, 0u};
+        if constexpr (EPI == OUT_GATED_GRAD) d = *reinterpret_cast<const uint2*>(stage + (32 * i + lr) * 80 + 4 * v0 + 8 * lh);
+#pragma unroll
+        for (int v = v0; v < v0 + 4; ++v) {
           float a, slope;
-          act_of<act.value>(acc[i][0][v], a, slope);
+          act_of<ACT>(acc[i][0][v], a, slope);
           if constexpr (EPI == OUT_GATED) {
             acc[i][0][v] = a * acc[i][1][v];
           } else {
-            const float dh = bf16f(*reinterpret_cast<const uint16_t*>(stage + (32 * i + 8 * (v >> 2) + 4 * lh + (v & 3)) * 80 + 2 * lr));
+            const uint32_t w = v - v0 < 2 ? d.x : d.y;
+            const float dh = __uint_as_float(v & 1 ? w & 0xFFFF0000u : w << 16);
             acc[i][0][v] = dh * acc[i][1][v] * slope;
             acc[i][1][v] = dh * a;
           }
-          if ((v & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // a few values' temporaries at a time
         }
-    };
-    if (g.act == W4A4_ACT_SILU)
-      apply(std::integral_constant<int, W4A4_ACT_SILU>{});
-    else
-      apply(std::integral_constant<int, W4A4_ACT_GELU>{});
+        __builtin_amdgcn_sched_barrier(0);   // a few values' temporaries at a time
+      }
     store_block<0, 1>(acc, stage, static_cast<uint16_t*>(g.out[0]), g.ldo, g.rows, g.cols, r0, c0, lane);
     if constexpr (EPI == OUT_GATED_GRAD)
       store_block<1, 1>(acc, stage, static_cast<uint16_t*>(g.out[1]), g.ldo, g.rows, g.cols, r0, c0, lane);
@@ -483,12 +489,12 @@ __global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16
 // ----------------------------------------------------------------------------- launch helpers
 inline int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
-template <int AM, int BM, int EPI>
+template <int AM, int BM, int EPI, int ACT = 0>
 hipError_t launch(const GemmArgs& g, hipStream_t st) {
   constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
-  const long long blocks = (long long)tiles_of(g.rows, TB) * g.probs * tiles_of(g.cols, GATED ? TB / 2 : TB);
+  const long long blocks = (long long)tiles_of(g.rows, TM) * g.probs * tiles_of(g.cols, GATED ? TN / 2 : TN);
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI>), dim3((unsigned)blocks, g.splits), dim3(GM_THREADS), 0, st, g);
+  hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI, ACT>), dim3((unsigned)blocks, g.splits), dim3(GM_THREADS), 0, st, g);
   return hipGetLastError();
 }
 
@@ -513,7 +519,7 @@ bool ld_ok(int ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= GM_MAX_
 // workspace of the backward pass: dG, dU [M][F] bf16, then the planes of dX's split contraction
 size_t gated_hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
 int gated_dx_splits(int M, int K, int F) {
-  return splits_of((long long)tiles_of(M, TB) * tiles_of(K, TB), 2 * tiles_of(F, KSTEP));
+  return splits_of((long long)tiles_of(M, TM) * tiles_of(K, TN), 2 * tiles_of(F, KSTEP));
 }
 
 }  // namespace
@@ -541,8 +547,8 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
     GemmArgs g{};
     g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = H;
     g.lda = ldx, g.ldb = ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
-    g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP), g.act = act;
-    e = launch<ROWS, ROWS, OUT_GATED>(g, st);
+    g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
+    e = act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_SILU>(g, st) : launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_GELU>(g, st);
   }
   return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
 }
@@ -570,8 +576,10 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
   GemmArgs g{};   // both projections again, then dG and dU rounded to bf16, the operands of what follows
   g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
   g.lda = ldx, g.ldb = ldw, g.ldo = F, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
-  g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP), g.act = act;
-  if (launch<ROWS, ROWS, OUT_GATED_GRAD>(g, st) != hipSuccess) return W4A4_ERR_HIP;
+  g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
+  if ((act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_SILU>(g, st)
+                            : launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_GELU>(g, st)) != hipSuccess)
+    return W4A4_ERR_HIP;
 
   GemmArgs x{};   // dX = [dG dU] [Wg; Wu]
   x.A[0] = dG, x.A[1] = dU, x.B[0] = Wg, x.B[1] = Wu;
@@ -589,7 +597,7 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
 }
 
 static int weight_grad_splits(int M, int N, int K) {
-  return splits_of((long long)tiles_of(N, TB) * tiles_of(K, TB), tiles_of(M, KSTEP));
+  return splits_of((long long)tiles_of(N, TM) * tiles_of(K, TN), tiles_of(M, KSTEP));
 }
 static bool weight_grad_shape_ok(int M, int N, int K) {
   return checkpoint_shape_ok(M, K) && N >= 8 && N % 8 == 0 && N <= GM_MAX_LD && K <= GM_MAX_LD;
