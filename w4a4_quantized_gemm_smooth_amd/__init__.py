@@ -48,6 +48,7 @@ _FMT_NAMES = {"int4_g64": FMT_INT4_G64, "mxfp4_b32": FMT_MXFP4_B32, "w8a8": FMT_
 _PKG = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_PKG, "libw4a4.so")
 _lib = None
+_torch = None   # set with _lib
 
 
 class W4A4Error(RuntimeError):
@@ -69,9 +70,10 @@ def lib() -> ctypes.CDLL:
 
     torch is imported first so that the library binds to the HIP runtime torch already loaded
     (one runtime per process; device pointers and streams are shared with torch)."""
-    global _lib
+    global _lib, _torch
     if _lib is None:
-        import torch  # noqa: F401  (loads the process's HIP runtime before libw4a4)
+        import torch  # (loads the process's HIP runtime before libw4a4)
+        _torch = torch
         if not os.path.exists(lib_path):
             raise ImportError(f"{lib_path} is missing: build it with "
                               "`python -m w4a4_quantized_gemm_smooth_amd.build` (no CPU fallback exists)")
@@ -428,16 +430,16 @@ def _check_bytes(name, t, nbytes, device):
 def _matrix(name, t):
     """Shape and device of the matrix that a call's other arguments go by; the kernels are launched on the
     current device, so it has to be there."""
-    import torch
     try:
         M, K = t.shape
         dev = t.device
     except (AttributeError, ValueError):
         raise ValueError(f"{name} must be a 2-D tensor") from None
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU (got {dev})")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    now = (_torch or lib() and _torch)._C._cuda_getDevice()
+    if dev.index != now:
+        raise ValueError(f"{name} is on {dev}, the current device is cuda:{now}")
     return M, K, dev
 
 
@@ -452,8 +454,7 @@ def _ptr(t):
 
 def _queue(stream, dev):
     """The given stream's handle, or that of the device's current stream."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=4096)
@@ -477,27 +478,27 @@ def matvec_sizes(M: int, N: int, K: int, rank: int, fmt=FMT_INT4_G64) -> dict:
 def matvec_weights(codes, scales, N, K, fmt, wv, stream=None):
     """Lay canonical codes [N, K/2] (uint8) and scales (INT4: [N, K/64] bf16; MXFP4: [N, K/32] uint8) out
     as ``matvec`` reads them; all on the GPU."""
-    import torch
     f = _fmt(fmt)
     _, _, dev = _matrix("codes", codes)
-    _check_tensor("codes", codes, torch.uint8, (N, K // 2), dev)
+    _check_tensor("codes", codes, _torch.uint8, (N, K // 2), dev)
     if f == FMT_INT4_G64:
-        _check_tensor("scales", scales, torch.bfloat16, (N, K // GROUP), dev)
+        _check_tensor("scales", scales, _torch.bfloat16, (N, K // GROUP), dev)
     else:
-        _check_tensor("scales", scales, torch.uint8, (N, K // MX_BLOCK), dev)
+        _check_tensor("scales", scales, _torch.uint8, (N, K // MX_BLOCK), dev)
     _check_bytes("wv", wv, matvec_sizes(1, N, K, 0, f)["wv"], dev)
-    _check("w4a4_matvec_weights", lib().w4a4_matvec_weights(_ptr(codes), _ptr(scales), N, K, f, _ptr(wv), _queue(stream, dev)))
+    st = _lib.w4a4_matvec_weights(_ptr(codes), _ptr(scales), N, K, f, _ptr(wv), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_matvec_weights", st)
 
 
 def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=None):
     """The layer for up to 16 rows of x [M, K] bf16 without quantizing them: y [M, N] bf16 (weight-only
     4-bit products, the low-rank branch and the bias; two kernels). ``wv`` from ``matvec_weights``."""
-    import torch
     f = _fmt(fmt)
     M, _, dev = _matrix("x", x)
     wv_bytes, ws_bytes = _two_sizes("w4a4_matvec_sizes", M, N, K, rank, f)
-    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
-    _check_tensor("y", y, torch.bfloat16, (M, N), dev, False)
+    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
+    _check_tensor("y", y, _torch.bfloat16, (M, N), dev, False)
     rp = (rank + RANK_ALIGN - 1) // RANK_ALIGN * RANK_ALIGN
     _check_bytes("inv_lambda", inv_lambda, 4 * K, dev)
     _check_bytes("wv", wv, wv_bytes, dev)
@@ -506,16 +507,17 @@ def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=Non
     _check_bytes("l2t", l2t, 2 * rp * N, dev)
     if bias is not None:
         _check_bytes("bias", bias, 2 * N, dev)
-    _check("w4a4_matvec", lib().w4a4_matvec(
+    st = _lib.w4a4_matvec(
         _ptr(x), M, K, _ld(x), _ptr(inv_lambda), _ptr(l1t), _ptr(wv), _ptr(l2t), _ptr(bias), _ptr(y), _ld(y), N, rank, f,
-        _ptr(ws), _queue(stream, dev)))
+        _ptr(ws), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_matvec", st)
 
 
 def _dtype(t, name):
-    import torch
-    if t is None or t.dtype == torch.bfloat16:
+    if t is None or t.dtype == _torch.bfloat16:
         return 0
-    if t.dtype != torch.float32:
+    if t.dtype != _torch.float32:
         raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
     return 1
 
@@ -531,17 +533,18 @@ def _norm_params(gamma, beta, K, dev):
 def layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=None):
     """y = (x - mean) rstd gamma + beta over the rows of x [M, K] (bf16 or fp32; gamma, beta [K] bf16, fp32
     or None), with the rows' mean and rstd [M] fp32 for ``layer_norm_backward``."""
-    import torch
     M, K, dev = _matrix("x", x)
     dt = _dtype(x, "x")
     _check_tensor("x", x, x.dtype, (M, K), dev, False)
     _check_tensor("y", y, x.dtype, (M, K), dev, False)
-    _check_tensor("mean", mean, torch.float32, (M,), dev)
-    _check_tensor("rstd", rstd, torch.float32, (M,), dev)
+    _check_tensor("mean", mean, _torch.float32, (M,), dev)
+    _check_tensor("rstd", rstd, _torch.float32, (M,), dev)
     pt = _norm_params(gamma, beta, K, dev)
-    _check("w4a4_layer_norm", lib().w4a4_layer_norm(
+    st = _lib.w4a4_layer_norm(
         _ptr(x), M, K, _ld(x), dt, _ptr(gamma), _ptr(beta), pt, eps, _ptr(y), _ld(y), _ptr(mean), _ptr(rstd),
-        _queue(stream, dev)))
+        _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_layer_norm", st)
 
 
 def layer_norm_backward_bytes(M: int, K: int) -> int:
@@ -551,21 +554,22 @@ def layer_norm_backward_bytes(M: int, K: int) -> int:
 def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
     """dx, and dgamma, dbeta [K] fp32 (either may be None; ``ws`` may be None where both are), of
     ``layer_norm`` from dy, x and the forward pass's mean and rstd."""
-    import torch
     M, K, dev = _matrix("x", x)
     dt = _dtype(x, "x")
     for name, t in (("dy", dy), ("x", x), ("dx", dx)):
         _check_tensor(name, t, x.dtype, (M, K), dev, False)
-    _check_tensor("mean", mean, torch.float32, (M,), dev)
-    _check_tensor("rstd", rstd, torch.float32, (M,), dev)
+    _check_tensor("mean", mean, _torch.float32, (M,), dev)
+    _check_tensor("rstd", rstd, _torch.float32, (M,), dev)
     for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
         if t is not None:
-            _check_tensor(name, t, torch.float32, (K,), dev)
+            _check_tensor(name, t, _torch.float32, (K,), dev)
     pt = _norm_params(gamma, None, K, dev)
     _check_bytes("ws", ws, 0 if dgamma is None and dbeta is None else layer_norm_backward_bytes(M, K), dev)
-    _check("w4a4_layer_norm_backward", lib().w4a4_layer_norm_backward(
+    st = _lib.w4a4_layer_norm_backward(
         _ptr(dy), _ld(dy), _ptr(x), _ld(x), dt, _ptr(gamma), pt, _ptr(mean), _ptr(rstd), M, K, _ptr(dx), _ld(dx),
-        _ptr(dgamma), _ptr(dbeta), _ptr(ws), _queue(stream, dev)))
+        _ptr(dgamma), _ptr(dbeta), _ptr(ws), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_layer_norm_backward", st)
 
 
 def checkpoint_sizes(M: int, K: int) -> dict:
@@ -582,22 +586,24 @@ def _check_checkpoint(codes, scales, M, K, dev):
 
 def checkpoint_pack(x, codes, scales, stream=None):
     """Keep x [M, K] bf16 in 8 bits: int8 codes and a power-of-two scale per channel and 32 tokens."""
-    import torch
     M, K, dev = _matrix("x", x)
-    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
+    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
     _check_checkpoint(codes, scales, M, K, dev)
-    _check("w4a4_checkpoint_pack", lib().w4a4_checkpoint_pack(
-        _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _queue(stream, dev)))
+    st = _lib.w4a4_checkpoint_pack(
+        _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_checkpoint_pack", st)
 
 
 def checkpoint_unpack(codes, scales, x, stream=None):
     """What the codes and scales stand for, into x [M, K] bf16 (exact)."""
-    import torch
     M, K, dev = _matrix("x", x)
-    _check_tensor("x", x, torch.bfloat16, (M, K), dev, False)
+    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
     _check_checkpoint(codes, scales, M, K, dev)
-    _check("w4a4_checkpoint_unpack", lib().w4a4_checkpoint_unpack(
-        _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x), _queue(stream, dev)))
+    st = _lib.w4a4_checkpoint_unpack(
+        _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_checkpoint_unpack", st)
 
 
 def checkpoint_weight_grad_bytes(M: int, N: int, K: int) -> int:
@@ -607,15 +613,16 @@ def checkpoint_weight_grad_bytes(M: int, N: int, K: int) -> int:
 def checkpoint_weight_grad(dy, codes, scales, K, dw, ws, stream=None):
     """dw [N, K] (fp32 or bf16) = dy^T x for dy [M, N] bf16 and the activations [M, K] kept in (codes,
     scales)."""
-    import torch
     M, N, dev = _matrix("dy", dy)
-    _check_tensor("dy", dy, torch.bfloat16, (M, N), dev, False)
+    _check_tensor("dy", dy, _torch.bfloat16, (M, N), dev, False)
     _check_checkpoint(codes, scales, M, K, dev)
     dt = _dtype(dw, "dw")
     _check_tensor("dw", dw, dw.dtype, (N, K), dev)
     _check_bytes("ws", ws, checkpoint_weight_grad_bytes(M, N, K), dev)
-    _check("w4a4_checkpoint_weight_grad", lib().w4a4_checkpoint_weight_grad(
-        _ptr(dy), _ld(dy), _ptr(codes), _ptr(scales), M, N, K, _ptr(dw), dt, _ptr(ws), _queue(stream, dev)))
+    st = _lib.w4a4_checkpoint_weight_grad(
+        _ptr(dy), _ld(dy), _ptr(codes), _ptr(scales), M, N, K, _ptr(dw), dt, _ptr(ws), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_checkpoint_weight_grad", st)
 
 
 def _act(act) -> int:
@@ -625,10 +632,9 @@ def _act(act) -> int:
 
 
 def _check_gated(x, wg, wu, h, name):
-    import torch
     M, K, dev = _matrix("x", x)
     F = _matrix("wg", wg)[0]
-    bf16 = torch.bfloat16
+    bf16 = _torch.bfloat16
     _check_tensor("x", x, bf16, (M, K), dev, False)
     _check_tensor("wg", wg, bf16, (F, K), dev, False)
     _check_tensor("wu", wu, bf16, (F, K), dev, False)
@@ -646,8 +652,10 @@ def gated_forward(x, wg, wu, act, h, ws=None, stream=None):
     """h [M, F] = act(x wg^T) * (x wu^T) for x [M, K], wg and wu [F, K], bf16; act "silu" or "gelu"."""
     M, K, F, dev = _check_gated(x, wg, wu, h, "h")
     _check_bytes("ws", ws, gated_forward_bytes(M, K, F), dev)
-    _check("w4a4_gated_forward", lib().w4a4_gated_forward(
-        _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(h), _ld(h), _ptr(ws), _queue(stream, dev)))
+    st = _lib.w4a4_gated_forward(
+        _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(h), _ld(h), _ptr(ws), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_gated_forward", st)
 
 
 def gated_backward_bytes(M: int, K: int, F: int) -> int:
@@ -656,14 +664,15 @@ def gated_backward_bytes(M: int, K: int, F: int) -> int:
 
 def gated_backward(dh, x, wg, wu, act, dx, dwg, dwu, ws, stream=None):
     """dx [M, K], dwg and dwu [F, K] (bf16) of ``gated_forward`` from dh [M, F] and its inputs."""
-    import torch
     M, K, F, dev = _check_gated(x, wg, wu, dh, "dh")
     for n, t, shape in (("dx", dx, (M, K)), ("dwg", dwg, (F, K)), ("dwu", dwu, (F, K))):
-        _check_tensor(n, t, torch.bfloat16, shape, dev)
+        _check_tensor(n, t, _torch.bfloat16, shape, dev)
     _check_bytes("ws", ws, gated_backward_bytes(M, K, F), dev)
-    _check("w4a4_gated_backward", lib().w4a4_gated_backward(
+    st = _lib.w4a4_gated_backward(
         _ptr(dh), _ld(dh), _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(dx), _ptr(dwg),
-        _ptr(dwu), _ptr(ws), _queue(stream, dev)))
+        _ptr(dwu), _ptr(ws), _queue(stream, dev))
+    if st:
+        raise W4A4Error("w4a4_gated_backward", st)
 
 
 class W4A4Linear:

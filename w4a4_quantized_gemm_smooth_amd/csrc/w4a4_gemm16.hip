@@ -437,6 +437,113 @@ __global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restric
     *reinterpret_cast<uint2*>(out + i) = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
 }
 
+// ------------------------------------------------- weight gradient of a few rows (a low-rank factor)
+// Up to 128 rows of dW: bound by reading the codes. A wave takes 64 channels and all rows; its lanes load a
+// token block's codes as the matrix operand needs them (16 of a channel's 32 tokens), and dY's 32 tokens go
+// through LDS for the transposing read. The eight waves of a block and the blocks of grid y take other token
+// blocks in turn, the next on its way under the current one; the waves' sums meet in LDS in order, the blocks' in
+// gemm16_join_kernel.
+constexpr int FG_WAVES = 8;
+template <int NT>   // 32-row tiles of dW
+__global__ __launch_bounds__(64 * FG_WAVES, NT == 1 ? 4 : 2) void factor_grad_kernel(const uint16_t* __restrict__ dY, int lddy,
+                                                          const uint8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ scales, int M, int N, int K,
+                                                          float* __restrict__ out) {
+  typedef __attribute__((address_space(3))) v4s* lds_v4s;
+  constexpr int RB = NT * 64, CPR = NT * 4, LOADS = NT * 2;   // bytes and 16-byte chunks of a token's row, loads a lane
+  constexpr int RED = FG_WAVES * 32 * 33 * 4;                 // a tile's sums [waves][32][32], a bank's shift a row
+  __shared__ __attribute__((aligned(16))) uint8_t lds[FG_WAVES * 32 * RB > RED ? FG_WAVES * 32 * RB : RED];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 31, lh = lane >> 5;
+  const int c0 = blockIdx.x * 64, nblk = (M + W4A4_CHECKPOINT_BLOCK - 1) / W4A4_CHECKPOINT_BLOCK, turn = FG_WAVES * gridDim.y;
+  uint8_t* mine = lds + wave * 32 * RB;
+  // chunk c of token row k at c ^ (k & 3 times as many chunks as a tile's half): other banks for the four
+  // rows of a read where the row has them
+  auto sw = [](int k) { return (NT >= 4 ? 4 * (k & 3) : NT == 2 ? 2 * (k & 3) : (k & 3)) & (CPR - 1); };
+  struct Block {   // a token block on its way
+    uint4 y[LOADS];
+    v4i q[2];
+    uint32_t e[2];
+  } on;
+  auto fetch = [&](int b, Block& o) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int at = i * 64 + lane, k = at / CPR, col = 8 * (at % CPR), tok = b * 32 + k;
+      o.y[i] = tok < M && col < N ? *reinterpret_cast<const uint4*>(dY + (size_t)tok * lddy + col) : uint4{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = c0 + 32 * j + lr;
+      const size_t at = (size_t)b * K + min(c, K - 1);
+      o.q[j] = *reinterpret_cast<const v4i*>(codes + at * 32 + 16 * lh);
+      o.e[j] = scales[at];
+    }
+  };
+  v16f acc[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  auto block = [&](int b, Block& o) {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int at = i * 64 + lane, k = at / CPR, c = at % CPR;
+      *reinterpret_cast<uint4*>(mine + k * RB + 16 * (c ^ sw(k))) = o.y[i];
+    }
+    v4i B[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float s = __uint_as_float(max(o.e[j] << 23, 0x00400000u));   // as in gemm16_kernel
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const uint32_t w = (uint32_t)o.q[j][d >> 1];
+        const int8_t a0 = (int8_t)(d & 1 ? w >> 16 : w), a1 = (int8_t)(d & 1 ? w >> 24 : w >> 8);
+        B[d >> 2][j][d & 3] = (int)pack_bf16x2((float)a0 * s, (float)a1 * s);
+      }
+    }
+    fetch(min(b + turn, nblk - 1), o);   // (the last one again past the end, unused)
+    const int i16 = lane & 15, mh = (lane >> 4) & 1;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        v2i a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = 16 * lh + 8 * s + 4 * h + (i16 >> 2), c = 4 * i + 2 * mh + ((i16 & 3) >> 1);
+          a[h] = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(mine + k * RB + 16 * (c ^ sw(k)) + 8 * (i16 & 1))));
+        }
+        const v4i A = v4i{a[0][0], a[0][1], a[1][0], a[1][1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(A), as_bf16x8(B[s][j]), acc[i][j], 0, 0, 0);
+      }
+  };
+  const int first = blockIdx.y * FG_WAVES + wave;
+  fetch(min(first, nblk - 1), on);
+#pragma unroll 1
+  for (int b = first; b < nblk; b += turn) block(b, on);
+  float* red = reinterpret_cast<float*>(lds);
+  float* plane = out + (size_t)blockIdx.y * N * K;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < 16; ++v) red[(wave * 32 + 8 * (v >> 2) + 4 * lh + (v & 3)) * 33 + lr] = acc[i][j][v];
+      __syncthreads();
+      for (int at = threadIdx.x; at < 32 * 32; at += 64 * FG_WAVES) {
+        const int n = at >> 5, c = at & 31, col = c0 + 32 * j + c;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < FG_WAVES; ++w) s += red[(32 * w + n) * 33 + c];
+        if (32 * i + n < N && col < K) plane[(size_t)(32 * i + n) * K + col] = s;
+      }
+    }
+}
+
 // ------------------------------------------------------------------- gated forward, 1 to 16 rows
 // A block takes 16 columns of H, its eight waves an eighth of the contraction each (interleaved by 64, so
 // the block reads whole lines of each weight row); X's operand comes straight from memory, where its few
@@ -596,7 +703,12 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
   return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
 }
 
+constexpr int FACTOR_MAX_N = 128;   // rows of dW up to which factor_grad_kernel is used
 static int weight_grad_splits(int M, int N, int K) {
+  if (N <= FACTOR_MAX_N) {   // a block to each compute unit, a token block at least to every wave
+    const int s = (256 + tiles_of(K, 64) - 1) / tiles_of(K, 64), most = tiles_of(tiles_of(M, W4A4_CHECKPOINT_BLOCK), FG_WAVES);
+    return s < most ? s : most;
+  }
   return splits_of((long long)tiles_of(N, TM) * tiles_of(K, TN), tiles_of(M, KSTEP));
 }
 static bool weight_grad_shape_ok(int M, int N, int K) {
@@ -621,7 +733,23 @@ w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const in
   g.lda = lddy, g.ldo = K, g.rows = N, g.cols = K, g.K = M;
   g.segs = g.probs = 1, g.steps = tiles_of(M, KSTEP), g.splits = weight_grad_splits(M, N, K);
   hipError_t e;
-  if (g.splits == 1) {
+  if (N <= FACTOR_MAX_N) {
+    float* planes = static_cast<float*>(ws);
+    const bool one = g.splits == 1 && out_dtype == W4A4_DTYPE_F32;
+    float* out = one ? static_cast<float*>(dW) : planes;
+    const dim3 grid(tiles_of(K, 64), g.splits);
+    const uint8_t* c = reinterpret_cast<const uint8_t*>(codes);
+    if (N <= 32)
+      hipLaunchKernelGGL(factor_grad_kernel<1>, grid, dim3(64 * FG_WAVES), 0, st, dY, lddy, c, scales, M, N, K, out);
+    else if (N <= 64)
+      hipLaunchKernelGGL(factor_grad_kernel<2>, grid, dim3(64 * FG_WAVES), 0, st, dY, lddy, c, scales, M, N, K, out);
+    else
+      hipLaunchKernelGGL(factor_grad_kernel<4>, grid, dim3(64 * FG_WAVES), 0, st, dY, lddy, c, scales, M, N, K, out);
+    e = hipGetLastError();
+    if (e == hipSuccess && !one)
+      e = out_dtype == W4A4_DTYPE_F32 ? join(planes, g.splits, (long long)N * K, static_cast<float*>(dW), st)
+                                      : join(planes, g.splits, (long long)N * K, static_cast<uint16_t*>(dW), st);
+  } else if (g.splits == 1) {
     g.out[0] = dW;
     e = out_dtype == W4A4_DTYPE_F32 ? launch<COLS, CODES, OUT_F32>(g, st) : launch<COLS, CODES, OUT_BF16>(g, st);
   } else {

@@ -32,7 +32,7 @@ constexpr int MV_WAVES = 8, MV_THREADS = 64 * MV_WAVES;
 constexpr int MV_MAX_M = W4A4_MATVEC_MAX_ROWS;
 constexpr int MV_TK = 2048;      // K of a block of the down projection: 256 a wave
 #ifndef W4A4_MV_TARGET           // build-time tuning knob: blocks aimed at
-#define W4A4_MV_TARGET 512
+#define W4A4_MV_TARGET 256
 #endif
 
 inline int mv_tiles(int N) { return (N + 15) / 16; }

@@ -82,36 +82,59 @@ __device__ __forceinline__ void store_piece(T* row, int k0, int K, const float (
   }
 }
 
-// the parameters of VEC<T> columns from k0 on (`none` where there are no parameters or no column)
+// The parameters of VEC<T> columns as they lie in memory (`none` in every element where there are no
+// parameters or no column), and element e of them.
 template <class T, class P>
-__device__ __forceinline__ void load_params(const P* p, int k0, int K, float none, float (&out)[VEC<T>]) {
+struct Params {
+  uint32_t w[VEC<T> * sizeof(P) / 4];
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(P) == 2)
+      return __uint_as_float((e & 1) ? (w[e >> 1] & 0xFFFF0000u) : (w[e >> 1] << 16));
+    else
+      return __uint_as_float(w[e]);
+  }
+};
+template <class T, class P>
+__device__ __forceinline__ Params<T, P> load_params(const P* p, int k0, int K, float none) {
+  constexpr int WORDS = VEC<T> * sizeof(P) / 4;
+  struct __attribute__((packed, aligned(sizeof(P)))) Raw { uint32_t w[WORDS]; };
+  Params<T, P> out;
+  const uint32_t f = __float_as_uint(none), fill = sizeof(P) == 2 ? (f >> 16) * 0x10001u : f;
 #pragma unroll
-  for (int e = 0; e < VEC<T>; ++e) out[e] = none;
-  if (!p) return;
+  for (int i = 0; i < WORDS; ++i) out.w[i] = fill;
+  if (!p) return out;
   if (k0 + VEC<T> <= K) {
-    constexpr int N = VEC<T> / VEC<P> > 0 ? VEC<T> / VEC<P> : 1;
-    if constexpr (VEC<T> >= VEC<P>) {
+    const Raw q = *reinterpret_cast<const Raw*>(p + k0);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const Piece<P> q = *reinterpret_cast<const Piece<P>*>(p + k0 + i * VEC<P>);
-#pragma unroll
-        for (int e = 0; e < VEC<P>; ++e) out[i * VEC<P> + e] = get<P>(q, e);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC<T>; ++e) out[e] = to_f(p[k0 + e]);
-    }
+    for (int i = 0; i < WORDS; ++i) out.w[i] = q.w[i];
   } else {
 #pragma unroll
     for (int e = 0; e < VEC<T>; ++e)
-      if (k0 + e < K) out[e] = to_f(p[k0 + e]);
+      if (k0 + e < K) {
+        if constexpr (sizeof(P) == 2) {
+          const uint32_t sh = 16 * (e & 1);
+          out.w[e >> 1] = (out.w[e >> 1] & ~(0xFFFFu << sh)) | (uint32_t)p[k0 + e] << sh;
+        } else {
+          out.w[e] = __float_as_uint(p[k0 + e]);
+        }
+      }
   }
+  return out;
 }
 
+// Sum over the wave, the same in every lane: within rows of 16 lanes by shifts, over the rows by the last
+// lanes' broadcasts; lane 63 then holds all.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+#define W4A4_DPP_ADD(ctrl, rows) \
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xF, true))
+  W4A4_DPP_ADD(0x111, 0xF);   // row_shr:1
+  W4A4_DPP_ADD(0x112, 0xF);   // row_shr:2
+  W4A4_DPP_ADD(0x114, 0xF);   // row_shr:4
+  W4A4_DPP_ADD(0x118, 0xF);   // row_shr:8
+  W4A4_DPP_ADD(0x142, 0xA);   // row_bcast:15 into rows 1 and 3
+  W4A4_DPP_ADD(0x143, 0xC);   // row_bcast:31 into rows 2 and 3
+#undef W4A4_DPP_ADD
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // Sums over the WPR waves that share a row, the same value in each of them. `red`: this call's own
@@ -192,9 +215,8 @@ __global__ __launch_bounds__(64 * WAVES) void norm_forward_kernel(const T* __res
   }
   auto write = [&](const Piece<T>& p, int k) {
     if (k >= K) return;
-    float g[V], b[V], o[V];
-    load_params<T, P>(gamma, k, K, 1.f, g);
-    load_params<T, P>(beta, k, K, 0.f, b);
+    const Params<T, P> g = load_params<T, P>(gamma, k, K, 1.f), b = load_params<T, P>(beta, k, K, 0.f);
+    float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = (get<T>(p, e) - mu) * rs * g[e] + b[e];
     store_piece<T>(y, k, K, o);
@@ -215,8 +237,9 @@ __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
     const float* __restrict__ mean, const float* __restrict__ rstd, int M, int K, T* __restrict__ dX, int lddx,
     float* __restrict__ part) {
   constexpr int G = WAVES / WPR, V = VEC<T>, STEP = 64 * WPR * V, CC = C > 0 ? C : 1;
+  constexpr bool AHEAD = WAVES <= 8;   // the next row's pieces on their way (blocks of 16 waves have no registers for them)
   __shared__ float red[2][G * WPR * 2];
-  extern __shared__ float cols[];   // [2][K], GRADS only
+  extern __shared__ __attribute__((aligned(16))) float cols[];   // [2][K up to a multiple of 4], GRADS only
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = wave / WPR, wr = wave % WPR;
   const int k0 = (wr * 64 + lane) * V;
   float dg[GRADS ? CC : 1][V] = {}, db[GRADS ? CC : 1][V] = {};
@@ -224,6 +247,11 @@ __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
   const long long first = (long long)blockIdx.x * G;   // every group makes the same number of turns
   int turn = 0;
   Piece<T> xv[CC], dv[CC];
+  Params<T, P> gam[CC];
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < CC; ++c) gam[c] = load_params<T, P>(gamma, k0 + c * STEP, K, 1.f);
+  }
   auto fetch = [&](long long base) {
     const long long row = base + group < M ? base + group : M - 1;
 #pragma unroll
@@ -239,17 +267,17 @@ __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
     const float mu = mean[row], rs = rstd[row];
     Piece<T> xc[CC], dc[CC];
     if constexpr (C > 0) {   // this row's data in hand, the next row's on its way
+      if (!AHEAD && base != first) fetch(base);
 #pragma unroll
       for (int c = 0; c < CC; ++c) {
         xc[c] = xv[c];
         dc[c] = dv[c];
       }
-      if (base + stride < M) fetch(base + stride);
+      if (AHEAD && base + stride < M) fetch(base + stride);
     }
     float s[2] = {0.f, 0.f};
     auto sums = [&](const Piece<T>& x, const Piece<T>& d, int k, int c) {
-      float g[V];
-      load_params<T, P>(gamma, k, K, 1.f, g);
+      const Params<T, P> g = C > 0 ? gam[c] : load_params<T, P>(gamma, k, K, 1.f);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float h = (get<T>(x, e) - mu) * rs, dy = get<T>(d, e), t = dy * g[e];   // dy is 0 past K
@@ -270,10 +298,10 @@ __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
     }
     row_sum<WPR, 2>(s, red[turn], group, wr, lane);
     const float m1 = s[0] / (float)K, m2 = s[1] / (float)K;
-    auto write = [&](const Piece<T>& x, const Piece<T>& d, int k) {
+    auto write = [&](const Piece<T>& x, const Piece<T>& d, int k, int c) {
       if (k >= K || !in) return;
-      float g[V], o[V];
-      load_params<T, P>(gamma, k, K, 1.f, g);
+      float o[V];
+      const Params<T, P> g = C > 0 ? gam[c] : load_params<T, P>(gamma, k, K, 1.f);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float h = (get<T>(x, e) - mu) * rs;
@@ -283,30 +311,40 @@ __global__ __launch_bounds__(64 * WAVES) void norm_backward_kernel(
     };
     if constexpr (C > 0) {
 #pragma unroll
-      for (int c = 0; c < CC; ++c) write(xc[c], dc[c], k0 + c * STEP);
+      for (int c = 0; c < CC; ++c) write(xc[c], dc[c], k0 + c * STEP, c);
     } else {
       for (int k = k0; k < K; k += STEP)
-        write(load_piece<T>(X + row * ldx, k, K), load_piece<T>(dY + row * lddy, k, K), k);
+        write(load_piece<T>(X + row * ldx, k, K), load_piece<T>(dY + row * lddy, k, K), k, 0);
     }
   }
-  if constexpr (GRADS) {   // the block's sums, its row groups in order
+  if constexpr (GRADS) {   // the block's sums, its row groups in order; columns past K hold zeros
+    const int Kp = (K + 3) & ~3;
     for (int g = 0; g < G; ++g) {
       if (group == g) {
 #pragma unroll
         for (int c = 0; c < CC; ++c)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
+          for (int e = 0; e < V; e += 4) {
             const int k = k0 + c * STEP + e;
-            if (k < K) {
-              cols[k] = g == 0 ? dg[c][e] : cols[k] + dg[c][e];
-              cols[K + k] = g == 0 ? db[c][e] : cols[K + k] + db[c][e];
+            if (k >= Kp) continue;
+            float4 *a = reinterpret_cast<float4*>(cols + k), *b = reinterpret_cast<float4*>(cols + Kp + k);
+            float4 u = {dg[c][e], dg[c][e + 1], dg[c][e + 2], dg[c][e + 3]}, v = {db[c][e], db[c][e + 1], db[c][e + 2], db[c][e + 3]};
+            if (g > 0) {
+              const float4 s = *a, t = *b;
+              u = float4{s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w};
+              v = float4{t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w};
             }
+            *a = u;
+            *b = v;
           }
       }
       __syncthreads();
     }
     float* out = part + (size_t)blockIdx.x * 2 * K;
-    for (int k = threadIdx.x; k < 2 * K; k += 64 * WAVES) out[k] = cols[k];
+    for (int k = threadIdx.x; k < K; k += 64 * WAVES) {
+      out[k] = cols[k];
+      out[K + k] = cols[Kp + k];
+    }
   }
 }
 
@@ -339,21 +377,22 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const T* __restrict__
   }
 }
 
-// dgamma, dbeta: the rows of part [rows][2][K] added in a fixed order; 16 lanes of a block's 1024
-// threads' columns each take every 16th row.
+// dgamma, dbeta: the rows of part [rows][2][K] added in a fixed order. A block takes 32 columns; thread (lane
+// of 32, w of 32) adds every 32nd row, then the 32 are added in order.
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part, int rows, int K,
                                                            float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float red[16][65];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = blockIdx.x * 64 + lane;
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (k < 2 * K) {
-#pragma unroll 16
-    for (int r = w; r < rows; r += 16) s += part[(size_t)r * 2 * K + k];
+#pragma unroll 8
+    for (int r = w; r < rows; r += 32) s += part[(size_t)r * 2 * K + k];
   }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && k < 2 * K) {
-    for (int i = 1; i < 16; ++i) s += red[i][lane];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) s += red[i][lane];
     if (k < K) {
       if (dgamma) dgamma[k] = s;
     } else if (dbeta) {
@@ -363,7 +402,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
 }
 
 // ----------------------------------------------------------------------------- launch helpers
-constexpr int NORM_BLOCKS = 256;      // backward: persistent blocks, one a compute unit
+constexpr int NORM_BLOCKS = 512;      // backward: persistent blocks, two a compute unit
 constexpr int NORM_MAX_K = 16384;     // longest row kept in registers
 
 template <class T, class P, int WPR, int C, int WAVES>
@@ -412,7 +451,7 @@ hipError_t backward(const void* dY, int lddy, const void* X, int ldx, const void
     hipLaunchKernelGGL((norm_columns_kernel<T>), dim3((K + 63) / 64, ry), dim3(256), 0, st, dy, lddy, x, ldx, mean, rstd, M, K, part);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 63) / 64), dim3(1024), 0, st, part, ry, K, dgamma, dbeta);
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 31) / 32), dim3(1024), 0, st, part, ry, K, dgamma, dbeta);
     return hipGetLastError();
   }
   const int blocks = need < NORM_BLOCKS ? need : NORM_BLOCKS;
@@ -421,7 +460,7 @@ hipError_t backward(const void* dY, int lddy, const void* X, int ldx, const void
                        ldx, static_cast<const P*>(gamma), mean, rstd, M, K, static_cast<T*>(dX), lddx, part);
     return hipGetLastError();
   }
-  const size_t lds = (size_t)2 * K * sizeof(float);
+  const size_t lds = (size_t)2 * ((K + 3) & ~3) * sizeof(float);
   if (lds > 32768) {   // longer rows: allow the block more than the default's dynamic LDS
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&norm_backward_kernel<T, P, WPR, C, WAVES, true>),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 2 * NORM_MAX_K * 4);
@@ -431,12 +470,13 @@ hipError_t backward(const void* dY, int lddy, const void* X, int ldx, const void
                      static_cast<const P*>(gamma), mean, rstd, M, K, static_cast<T*>(dX), lddx, part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 63) / 64), dim3(1024), 0, st, part, blocks, K, dgamma, dbeta);
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((2 * K + 31) / 32), dim3(1024), 0, st, part, blocks, K, dgamma, dbeta);
   return hipGetLastError();
 }
 
-// Row groups of 1, 4 and 16 waves: a thread holds two rows' pieces (the current and the next) and the
-// sums of its columns, so at most 2 (16-bit) or 4 (32-bit) pieces keep it in its registers.
+// A thread holds two rows' pieces (the current and the next) and the sums of its columns. A block is one
+// row's waves where that is more than one: blocks of several rows waited for each other's barriers (bf16
+// 16384 x 4096, two blocks a compute unit: four rows a block 116 us, two 89, one 84).
 template <class T, class P>
 hipError_t dispatch_backward(const void* dY, int lddy, const void* X, int ldx, const void* gamma, const float* mean,
                              const float* rstd, int M, int K, void* dX, int lddx, float* dgamma, float* dbeta, float* part,
@@ -444,11 +484,12 @@ hipError_t dispatch_backward(const void* dY, int lddy, const void* X, int ldx, c
   constexpr int W = 64 * VEC<T>;
 #define W4A4_NB(wpr, c, waves) \
   return backward<T, P, wpr, c, waves>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st)
-  if (K <= W) W4A4_NB(1, 1, 16);
-  if (K <= 4 * W) W4A4_NB(4, 1, 16);
-  if (K <= 8 * W) W4A4_NB(4, 2, 16);
-  if (K <= 16 * W) W4A4_NB(16, 1, 16);
-  if (K <= 32 * W) W4A4_NB(16, 2, 16);
+  if (K <= W) W4A4_NB(1, 1, 8);
+  if (K <= 2 * W) W4A4_NB(1, 2, 8);
+  if (K <= 4 * W) W4A4_NB(1, 4, 8);
+  if (K <= 8 * W) W4A4_NB(4, 2, 4);
+  if (K <= 16 * W) W4A4_NB(8, 2, 8);
+  if (K <= 32 * W) W4A4_NB(8, 4, 8);
   if constexpr (sizeof(T) == 4)
     if (K <= 64 * W) W4A4_NB(16, 4, 16);
   W4A4_NB(4, 0, 4);
