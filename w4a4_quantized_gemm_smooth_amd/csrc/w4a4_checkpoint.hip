@@ -11,8 +11,9 @@
 // contraction runs along them, so its matrix operand is 8 consecutive bytes), scales [ceil(M/32)][K]
 // bytes e + 127; 255 marks a block that holds an Inf or NaN, whose values all read back as NaN.
 //
-// Both kernels move each byte once; a thread owns 4 channels of a block: 32 loads (or stores) of 8
-// bytes down the tokens, one 128-byte line of codes.
+// Both kernels move each byte once and are bound by that; a thread owns 4 channels of a block: 32 loads
+// (or stores) of 8 bytes down the tokens, one 128-byte line of codes. Packing passes the lines through LDS,
+// so that a wave stores whole KBs instead of 16 bytes of 64 lines at a time (4608 x 12288: 47 us without).
 #include "w4a4_device_common.h"
 
 using namespace w4a4;
@@ -22,6 +23,7 @@ namespace {
 
 constexpr int CK_CH = 4;        // channels per thread
 constexpr int CK_THREADS = 256;
+constexpr int CK_LINE = CK_CH * W4A4_CHECKPOINT_BLOCK + 16;   // a line in LDS: 16 bytes more, other banks for the next
 
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
@@ -36,9 +38,10 @@ __global__ __launch_bounds__(CK_THREADS) void checkpoint_pack_kernel(const uint1
                                                                      int8_t* __restrict__ codes,
                                                                      uint8_t* __restrict__ scales) {
   const int nk = (K + CK_CH * CK_THREADS - 1) / (CK_CH * CK_THREADS), b = blockIdx.x / nk;
-  const int k = (blockIdx.x % nk * CK_THREADS + threadIdx.x) * CK_CH;
-  if (k >= K) return;
-  const int rows = min(W4A4_CHECKPOINT_BLOCK, M - b * W4A4_CHECKPOINT_BLOCK);
+  const int k = (blockIdx.x % nk * CK_THREADS + threadIdx.x) * CK_CH, lane = threadIdx.x & 63;
+  __shared__ __attribute__((aligned(16))) uint8_t lines[CK_THREADS / 64][64 * CK_LINE];   // a wave's own
+  uint8_t* mine = lines[threadIdx.x >> 6];
+  const int rows = k < K ? min(W4A4_CHECKPOINT_BLOCK, M - b * W4A4_CHECKPOINT_BLOCK) : 0;
   const uint16_t* x = X + (size_t)b * W4A4_CHECKPOINT_BLOCK * ldx + k;
   uint2 v[W4A4_CHECKPOINT_BLOCK];
 #pragma unroll
@@ -52,7 +55,7 @@ __global__ __launch_bounds__(CK_THREADS) void checkpoint_pack_kernel(const uint1
     ty = __builtin_elementwise_max(ty, __builtin_bit_cast(us2, v[r].y & 0x7FFF7FFFu));
   }
   uint32_t bytes = 0u;
-  uint4* out = reinterpret_cast<uint4*>(codes + ((size_t)b * K + k) * W4A4_CHECKPOINT_BLOCK);
+  uint4* out = reinterpret_cast<uint4*>(mine + lane * CK_LINE);
 #pragma unroll
   for (int c = 0; c < CK_CH; ++c) {
     const uint32_t top = c < 2 ? tx[c & 1] : ty[c & 1];
@@ -84,7 +87,16 @@ __global__ __launch_bounds__(CK_THREADS) void checkpoint_pack_kernel(const uint1
     out[2 * c] = uint4{w[0], w[1], w[2], w[3]};
     out[2 * c + 1] = uint4{w[4], w[5], w[6], w[7]};
   }
-  *reinterpret_cast<uint32_t*>(scales + (size_t)b * K + k) = bytes;
+  if (k < K) *reinterpret_cast<uint32_t*>(scales + (size_t)b * K + k) = bytes;
+  // the wave's lines, 8 pieces of 16 bytes each, piece after piece (one wave's LDS accesses stay in order)
+  const int k0 = k - lane * CK_CH;
+  uint4* dst = reinterpret_cast<uint4*>(codes + ((size_t)b * K + k0) * W4A4_CHECKPOINT_BLOCK);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = i * 64 + lane, line = at >> 3;
+    const uint4 v = *reinterpret_cast<const uint4*>(mine + line * CK_LINE + 16 * (at & 7));
+    if (k0 + line * CK_CH < K) dst[at] = v;
+  }
 }
 
 __global__ __launch_bounds__(CK_THREADS) void checkpoint_unpack_kernel(const int8_t* __restrict__ codes,
