@@ -426,7 +426,8 @@ def test_checkpoint_of_every_bf16_value():
 @gpu
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (31, 8, 64), (33, 264, 40), (64, 256, 256), (97, 40, 520), (300, 520, 264), (2049, 16, 1000),
-                                   (1500, 128, 136), (1000, 136, 8), (5000, 32, 72)])
+                                   (1500, 128, 136), (1000, 136, 8), (5000, 32, 72), (2100, 64, 520),
+                                   (700, 72, 200), (1000, 200, 72)])
 def test_checkpoint_weight_grad(M, N, K, out):
     x, dy = _rand(M, (M, K)), _rand(N, (M, N), 0.1)
     codes, scales = _pack(x)
@@ -501,8 +502,8 @@ def _gated_backward(x, wg, wu, dh, act):
     return dx, dwg, dwu
 
 
-GATED = [(1, 8, 8), (1, 512, 200), (2, 72, 40), (16, 1032, 264), (17, 40, 136), (33, 200, 72), (255, 64, 128), (300, 520, 392), (64, 2048, 1000),
-         (513, 96, 24)]
+GATED = [(1, 8, 8), (1, 512, 200), (2, 72, 40), (16, 1032, 264), (17, 40, 136), (33, 200, 72), (48, 136, 520), (49, 64, 64), (255, 64, 128), (300, 520, 392), (64, 2048, 1000),
+         (513, 96, 24), (2000, 256, 256)]
 
 
 @gpu

@@ -4,8 +4,8 @@
 //     dG = dH (.) U (.) act'(G),  dU = dH (.) act(G)                      (the same kernel's other epilogue)
 //     dX = dG Wg + dU Wu,  dWg = dG^T X,  dWu = dU^T X,
 // and the weight gradient dW = dY^T X~ from activations kept in 8 bits (w4a4_checkpoint.hip).
-// One row of X at a time (1 to 16 tokens) the forward pass is bound by reading the weights and has a
-// kernel of its own.
+// For a few rows of X (single tokens) the forward pass is bound by reading the weights and has a kernel of
+// its own.
 //
 // The product kernel. Blocks of 256 x 256 outputs, eight waves of 128 x 64 (4 x 2 tiles of 32x32, 128
 // accumulators to a lane). A step is 32 of the contraction: 16 KB an operand in one of four ring slots in
@@ -418,11 +418,15 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   }
 }
 
-// The planes of a split contraction added in order: out[i] = sum_s part[s][i], fp32 or rounded to bf16.
+// The planes of a split contraction added in order: out[i] = sum_s part[s][i], fp32 or rounded to bf16; for
+// grid y = 1 the second product's, whose planes follow the first's.
 template <class T>
-__global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restrict__ part, int splits, long long n, T* __restrict__ out) {
+__global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restrict__ part, int splits, long long n,
+                                                          T* __restrict__ out0, T* __restrict__ out1) {
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;   // n is a multiple of 8
+  part += blockIdx.y * splits * n;
+  T* out = blockIdx.y ? out1 : out0;
   float4 s = *reinterpret_cast<const float4*>(part + i);
   for (int q = 1; q < splits; ++q) {
     const float4 v = *reinterpret_cast<const float4*>(part + q * n + i);
@@ -544,53 +548,76 @@ __global__ __launch_bounds__(64 * FG_WAVES, NT == 1 ? 4 : 2) void factor_grad_ke
     }
 }
 
-// ------------------------------------------------------------------- gated forward, 1 to 16 rows
-// A block takes 16 columns of H, its eight waves an eighth of the contraction each (interleaved by 64, so
-// the block reads whole lines of each weight row); X's operand comes straight from memory, where its few
-// rows stay in the caches. The waves' sums meet in LDS in wave order. Lane (r = lane % 16, j = lane / 16)
-// takes the contraction 64 i + 16 j + 0..15 of weight row r and of X row r in two operands.
-constexpr int GT_WAVES = 8;
+// ------------------------------------------------------------------- gated forward, 1 to 48 rows
+// Bound by reading the weights. A block takes 16 columns of H, its eight waves an eighth of the contraction
+// each (interleaved by 64, so the block reads whole lines of each weight row); X's operands (MT tiles of 16
+// rows) come straight from memory, where its few rows stay in the caches. The waves' sums meet in LDS, four
+// and four, in wave order. Lane (r = lane % 16, j = lane / 16) takes the contraction 64 i + 16 j + 0..15 of
+// weight row r and of X row r in two operands. (4096 x 12288: 1 row 43 us, 16 rows 50, 32 rows 59, where the
+// product kernel takes 80; with 32 columns a block 72 for 32 rows; at 64 rows both take 81 to 86.)
+constexpr int GT_WAVES = 8, GT_MAX_M = 48;
+template <int MT>
 __global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16_t* __restrict__ X, int M, int K, int ldx,
                                                                     const uint16_t* __restrict__ Wg,
                                                                     const uint16_t* __restrict__ Wu, int ldw, int F, int act,
                                                                     uint16_t* __restrict__ H, int ldh) {
-  __shared__ __attribute__((aligned(16))) float red[GT_WAVES][2][16][16];
+  __shared__ __attribute__((aligned(16))) float red[GT_WAVES / 2][2][MT * 16][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, j = lane >> 4;
   const int f = min(blockIdx.x * 16 + r, F - 1);   // rows past the end repeat the last one
-  const uint16_t *wg = Wg + (size_t)f * ldw, *wu = Wu + (size_t)f * ldw, *x = X + (size_t)min(r, M - 1) * ldx;
+  const uint16_t *wg = Wg + (size_t)f * ldw, *wu = Wu + (size_t)f * ldw, *x[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = X + (size_t)min(16 * m + r, M - 1) * ldx;
   const v4i zero = {0, 0, 0, 0};
-  v4f ag = {0.f, 0.f, 0.f, 0.f}, au = ag;
+  v4f acc[2][MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[0][m] = acc[1][m] = v4f{0.f, 0.f, 0.f, 0.f};
   for (int k0 = 64 * wave; k0 < K; k0 += 64 * GT_WAVES) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int k = k0 + 16 * j + 8 * s;
       const bool in = k < K;   // K is a multiple of 8
-      const v4i a = in && r < M ? *reinterpret_cast<const v4i*>(x + k) : zero;
-      const v4i b = in ? *reinterpret_cast<const v4i*>(wg + k) : zero, c = in ? *reinterpret_cast<const v4i*>(wu + k) : zero;
-      ag = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), ag, 0, 0, 0);
-      au = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(c), au, 0, 0, 0);
+      v4i a[MT];
+      const v4i b[2] = {in ? *reinterpret_cast<const v4i*>(wg + k) : zero, in ? *reinterpret_cast<const v4i*>(wu + k) : zero};
+#pragma unroll
+      for (int m = 0; m < MT; ++m) a[m] = in && 16 * m + r < M ? *reinterpret_cast<const v4i*>(x[m] + k) : zero;
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[w][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a[m]), as_bf16x8(b[w]), acc[w][m], 0, 0, 0);
     }
   }
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    red[wave][0][4 * j + v][r] = ag[v];
-    red[wave][1][4 * j + v][r] = au[v];
-  }
-  __syncthreads();
-  const int m = threadIdx.x >> 4, c = threadIdx.x & 15, col = blockIdx.x * 16 + c;
-  if (m >= M || col >= F) return;   // threads 0..255 of 512 have a row below 16
-  float gs = 0.f, us = 0.f;
+  for (int half = 1; half >= 0; --half) {   // waves 4..7, then 0..3 on top
+    if (wave / 4 == half) {
 #pragma unroll
-  for (int w = 0; w < GT_WAVES; ++w) {
-    gs += red[w][0][m][c];
-    us += red[w][1][m][c];
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            float* p = &red[wave & 3][w][16 * m + 4 * j + v][r];
+            *p = half ? acc[w][m][v] : *p + acc[w][m][v];
+          }
+    }
+    __syncthreads();
   }
-  float a, slope;
-  if (act == W4A4_ACT_SILU)
-    act_of<W4A4_ACT_SILU>(gs, a, slope);
-  else
-    act_of<W4A4_ACT_GELU>(gs, a, slope);
-  H[(size_t)m * ldh + col] = (uint16_t)pack_bf16x2(a * us, 0.f);
+  for (int i = threadIdx.x; i < M * 16; i += 64 * GT_WAVES) {
+    const int m = i >> 4, c = i & 15, col = blockIdx.x * 16 + c;
+    if (col >= F) continue;
+    float gs = 0.f, us = 0.f;
+#pragma unroll
+    for (int w = 0; w < GT_WAVES / 2; ++w) {
+      gs += red[w][0][m][c];
+      us += red[w][1][m][c];
+    }
+    float a, slope;
+    if (act == W4A4_ACT_SILU)
+      act_of<W4A4_ACT_SILU>(gs, a, slope);
+    else
+      act_of<W4A4_ACT_GELU>(gs, a, slope);
+    H[(size_t)m * ldh + col] = (uint16_t)pack_bf16x2(a * us, 0.f);
+  }
 }
 
 // ----------------------------------------------------------------------------- launch helpers
@@ -606,16 +633,27 @@ hipError_t launch(const GemmArgs& g, hipStream_t st) {
 }
 
 template <class T>
-hipError_t join(const float* part, int splits, long long n, T* out, hipStream_t st) {
-  hipLaunchKernelGGL((gemm16_join_kernel<T>), dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, part, splits, n, out);
+hipError_t join(const float* part, int splits, long long n, T* out, hipStream_t st, T* second = nullptr) {
+  hipLaunchKernelGGL((gemm16_join_kernel<T>), dim3((unsigned)((n / 4 + 255) / 256), second ? 2 : 1), dim3(256), 0, st, part, splits, n,
+                     out, second);
   return hipGetLastError();
 }
 
-// Parts of the contraction: as many as give every compute unit a block, each at least 8 steps long.
-int splits_of(long long blocks, int steps) {
-  long long s = 256 / blocks;
-  if (s > steps / 8) s = steps / 8;
-  return s < 1 ? 1 : (int)s;
+// Parts of the contraction, so that a few blocks fill the chip: the number that a simple cost favours.
+// Measured: a step of a round of 256 blocks 0.6 us (0.9 where the chip's power limits it: all blocks at
+// length); a value of a plane, written and read by the join, 8 bytes at 6 TB/s, and 6 us for the join's
+// launch. Parts are at least 4 steps long.
+int splits_of(long long blocks, int steps, double values) {
+  int best = 1;
+  double least = 0.;
+  for (int s = 1; s == 1 || (s <= steps / 4 && s <= 64 && blocks * s <= 512); ++s) {
+    const double t = 0.6 * (double)((blocks * s + 255) / 256) * ((steps + s - 1) / s) + (s > 1 ? 6. + s * values * 8. / 6e6 : 0.);
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
 
 bool gated_shape_ok(int M, int K, int F) {
@@ -623,10 +661,14 @@ bool gated_shape_ok(int M, int K, int F) {
 }
 bool ld_ok(int ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= GM_MAX_LD; }
 
-// workspace of the backward pass: dG, dU [M][F] bf16, then the planes of dX's split contraction
+// workspace of the backward pass: dG, dU [M][F] bf16, then the planes of a split contraction (dX's, then the
+// two weights')
 size_t gated_hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
 int gated_dx_splits(int M, int K, int F) {
-  return splits_of((long long)tiles_of(M, TM) * tiles_of(K, TN), 2 * tiles_of(F, KSTEP));
+  return splits_of((long long)tiles_of(M, TM) * tiles_of(K, TN), 2 * tiles_of(F, KSTEP), (double)M * K);
+}
+int gated_dw_splits(int M, int K, int F) {
+  return splits_of(2LL * tiles_of(F, TM) * tiles_of(K, TN), tiles_of(M, KSTEP), 2. * F * K);
 }
 
 }  // namespace
@@ -647,8 +689,14 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
   if (!X || !Wg || !Wu || !H || !aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H)) return W4A4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t e;
-  if (M <= 16) {
-    hipLaunchKernelGGL(gated_token_kernel, dim3(tiles_of(F, 16)), dim3(64 * GT_WAVES), 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
+  if (M <= GT_MAX_M) {
+    const dim3 grid(tiles_of(F, 16)), block(64 * GT_WAVES);
+    if (M <= 16)
+      hipLaunchKernelGGL(gated_token_kernel<1>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
+    else if (M <= 32)
+      hipLaunchKernelGGL(gated_token_kernel<2>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
+    else
+      hipLaunchKernelGGL(gated_token_kernel<3>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
     e = hipGetLastError();
   } else {
     GemmArgs g{};
@@ -662,8 +710,9 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
 
 size_t w4a4_gated_backward_bytes(int M, int K, int F) {
   if (!gated_shape_ok(M, K, F)) return 0;
-  const int sp = gated_dx_splits(M, K, F);
-  return 2 * gated_hidden_bytes(M, F) + (sp > 1 ? (size_t)sp * M * K * 4 : 0);
+  const int sx = gated_dx_splits(M, K, F), sw = gated_dw_splits(M, K, F);
+  const size_t px = sx > 1 ? (size_t)sx * M * K * 4 : 0, pw = sw > 1 ? (size_t)sw * 2 * F * K * 4 : 0;
+  return 2 * gated_hidden_bytes(M, F) + (px > pw ? px : pw);
 }
 
 w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg,
@@ -699,8 +748,12 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
   GemmArgs w{};   // dWg = dG^T X, dWu = dU^T X
   w.A[0] = dG, w.A[1] = dU, w.B[0] = X, w.out[0] = dWg, w.out[1] = dWu;
   w.lda = F, w.ldb = ldx, w.ldo = K, w.rows = F, w.cols = K, w.K = M;
-  w.segs = 1, w.probs = 2, w.splits = 1, w.steps = tiles_of(M, KSTEP);
-  return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+  w.segs = 1, w.probs = 2, w.splits = gated_dw_splits(M, K, F), w.steps = tiles_of(M, KSTEP);
+  if (w.splits == 1) return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+  const long long n = (long long)F * K;
+  w.out[0] = planes, w.out[1] = planes + w.splits * n;
+  const bool ok = launch<COLS, COLS, OUT_F32>(w, st) == hipSuccess && join(planes, w.splits, n, dWg, st, dWu) == hipSuccess;
+  return ok ? W4A4_OK : W4A4_ERR_HIP;
 }
 
 constexpr int FACTOR_MAX_N = 128;   // rows of dW up to which factor_grad_kernel is used
@@ -709,7 +762,7 @@ static int weight_grad_splits(int M, int N, int K) {
     const int s = (256 + tiles_of(K, 64) - 1) / tiles_of(K, 64), most = tiles_of(tiles_of(M, W4A4_CHECKPOINT_BLOCK), FG_WAVES);
     return s < most ? s : most;
   }
-  return splits_of((long long)tiles_of(N, TM) * tiles_of(K, TN), tiles_of(M, KSTEP));
+  return splits_of((long long)tiles_of(N, TM) * tiles_of(K, TN), tiles_of(M, KSTEP), (double)N * K);
 }
 static bool weight_grad_shape_ok(int M, int N, int K) {
   return checkpoint_shape_ok(M, K) && N >= 8 && N % 8 == 0 && N <= GM_MAX_LD && K <= GM_MAX_LD;
