@@ -503,7 +503,7 @@ def _gated_backward(x, wg, wu, dh, act):
 
 
 GATED = [(1, 8, 8), (1, 512, 200), (2, 72, 40), (16, 1032, 264), (17, 40, 136), (33, 200, 72), (48, 136, 520), (49, 64, 64), (255, 64, 128), (300, 520, 392), (64, 2048, 1000),
-         (513, 96, 24), (2000, 256, 256)]
+         (513, 96, 24), (2000, 256, 256), (1100, 2056, 1032)]
 
 
 @gpu

@@ -441,6 +441,24 @@ __global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restric
     *reinterpret_cast<uint2*>(out + i) = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
 }
 
+// Rows that do not start at multiples of 64 bytes take the copies by ROWS twice the lines (2041 x 2056 x 5624,
+// the gradients' first product: 2960 cycles a step against 1440), far more than laying them out anew once:
+// up to three matrices of the same width -> rows of ldp elements, in 16-byte pieces.
+struct PadArgs {
+  const uint16_t* src[3];
+  uint16_t* dst[3];
+  int ld[3], rows[3], cols, ldp;
+};
+__global__ __launch_bounds__(256) void pad_rows_kernel(const PadArgs a) {
+  const int y = blockIdx.y, per = a.ldp / 8;
+  const long long n = (long long)a.rows[y] * per, stride = (long long)gridDim.x * 256;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
+    const long long row = i / per;
+    const int c = (int)(i - row * per) * 8;
+    if (c < a.cols) *reinterpret_cast<uint4*>(a.dst[y] + row * a.ldp + c) = *reinterpret_cast<const uint4*>(a.src[y] + row * a.ld[y] + c);
+  }
+}
+
 // ------------------------------------------------- weight gradient of a few rows (a low-rank factor)
 // Up to 128 rows of dW: bound by reading the codes. A wave takes 64 channels and all rows; its lanes load a
 // token block's codes as the matrix operand needs them (16 of a channel's 32 tokens), and dY's 32 tokens go
@@ -661,9 +679,44 @@ bool gated_shape_ok(int M, int K, int F) {
 }
 bool ld_ok(int ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= GM_MAX_LD; }
 
-// workspace of the backward pass: dG, dU [M][F] bf16, then the planes of a split contraction (dX's, then the
-// two weights')
-size_t gated_hidden_bytes(int M, int F) { return ((size_t)M * F * 2 + 255) / 256 * 256; }
+// Workspace: for large products whose K is no multiple of 32, room for X, Wg and Wu with rows of a multiple of
+// 64 bytes; for the backward pass then dG, dU [M][F up to a multiple of 32] bf16, and the planes of a split
+// contraction (dX's, then the two weights').
+inline int pad32(int n) { return (n + 31) / 32 * 32; }
+size_t matrix_bytes(int rows, int cols) { return ((size_t)rows * pad32(cols) * 2 + 255) / 256 * 256; }
+// Only where the steps' extra time (measured: 0.35 us a step of a round of 256 blocks) clearly exceeds the copy's.
+size_t gated_pad_bytes(int M, int K, int F) {
+  if (K % 32 == 0 || M <= GT_MAX_M) return 0;
+  const double rounds = (double)(((long long)tiles_of(M, TM) * tiles_of(F, TN / 2) + 255) / 256);
+  const double extra = 0.35 * rounds * tiles_of(K, KSTEP), copy = 6. + ((double)M + 2. * F) * K * 4. / 5e6;
+  return extra < 1.3 * copy ? 0 : matrix_bytes(M, K) + 2 * matrix_bytes(F, K);
+}
+size_t gated_hidden_bytes(int M, int F) { return matrix_bytes(M, F); }
+
+// X, Wg and Wu as the products read them: laid out anew in ws where that has room and their rows need it
+struct GatedOperands {
+  const uint16_t *x, *wg, *wu;
+  int ldx, ldw;
+};
+hipError_t gated_operands(const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg, const uint16_t* Wu, int ldw, int F, void* ws,
+                          GatedOperands& o, hipStream_t st) {
+  o = {X, Wg, Wu, ldx, ldw};
+  auto fine = [](const void* p, int ld) { return (reinterpret_cast<uintptr_t>(p) & 63u) == 0 && ld % 32 == 0; };
+  if (gated_pad_bytes(M, K, F) == 0 || (fine(X, ldx) && fine(Wg, ldw) && fine(Wu, ldw))) return hipSuccess;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  const int ldp = pad32(K);
+  PadArgs a{};
+  a.src[0] = X, a.src[1] = Wg, a.src[2] = Wu;
+  a.ld[0] = ldx, a.ld[1] = a.ld[2] = ldw;
+  a.rows[0] = M, a.rows[1] = a.rows[2] = F;
+  a.dst[0] = reinterpret_cast<uint16_t*>(p);
+  a.dst[1] = reinterpret_cast<uint16_t*>(p + matrix_bytes(M, K));
+  a.dst[2] = reinterpret_cast<uint16_t*>(p + matrix_bytes(M, K) + matrix_bytes(F, K));
+  a.cols = K, a.ldp = ldp;
+  o = {a.dst[0], a.dst[1], a.dst[2], ldp, ldp};
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(1024, 3), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
 int gated_dx_splits(int M, int K, int F) {
   return splits_of((long long)tiles_of(M, TM) * tiles_of(K, TN), 2 * tiles_of(F, KSTEP), (double)M * K);
 }
@@ -677,16 +730,15 @@ int gated_dw_splits(int M, int K, int F) {
 extern "C" {
 
 size_t w4a4_gated_forward_bytes(int M, int K, int F) {
-  (void)M, (void)K, (void)F;
-  return 0;
+  return gated_shape_ok(M, K, F) ? gated_pad_bytes(M, K, F) : 0;
 }
 
 w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg, const uint16_t* Wu, int ldw,
                                  int F, int act, uint16_t* H, int ldh, void* ws, w4a4_stream_t stream) {
-  (void)ws;
   if (act != W4A4_ACT_SILU && act != W4A4_ACT_GELU) return W4A4_ERR_UNSUPPORTED;
   if (!gated_shape_ok(M, K, F) || !ld_ok(ldx, K) || !ld_ok(ldw, K) || !ld_ok(ldh, F)) return W4A4_ERR_INVALID_ARG;
   if (!X || !Wg || !Wu || !H || !aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H)) return W4A4_ERR_INVALID_ARG;
+  if (gated_pad_bytes(M, K, F) > 0 && (!ws || !aligned16(ws))) return W4A4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t e;
   if (M <= GT_MAX_M) {
@@ -699,9 +751,12 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
       hipLaunchKernelGGL(gated_token_kernel<3>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
     e = hipGetLastError();
   } else {
+    GatedOperands o;
+    e = gated_operands(X, M, K, ldx, Wg, Wu, ldw, F, ws, o, st);
+    if (e != hipSuccess) return W4A4_ERR_HIP;
     GemmArgs g{};
-    g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = H;
-    g.lda = ldx, g.ldb = ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
+    g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = H;
+    g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
     g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
     e = act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_SILU>(g, st) : launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_GELU>(g, st);
   }
@@ -712,7 +767,7 @@ size_t w4a4_gated_backward_bytes(int M, int K, int F) {
   if (!gated_shape_ok(M, K, F)) return 0;
   const int sx = gated_dx_splits(M, K, F), sw = gated_dw_splits(M, K, F);
   const size_t px = sx > 1 ? (size_t)sx * M * K * 4 : 0, pw = sw > 1 ? (size_t)sw * 2 * F * K * 4 : 0;
-  return 2 * gated_hidden_bytes(M, F) + (px > pw ? px : pw);
+  return gated_pad_bytes(M, K, F) + 2 * gated_hidden_bytes(M, F) + (px > pw ? px : pw);
 }
 
 w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg,
@@ -725,29 +780,33 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
       !aligned16(dWu) || !aligned16(ws))
     return W4A4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  uint16_t* dG = static_cast<uint16_t*>(ws);
-  uint16_t* dU = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + gated_hidden_bytes(M, F));
-  float* planes = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 2 * gated_hidden_bytes(M, F));
+  uint8_t* p = static_cast<uint8_t*>(ws) + gated_pad_bytes(M, K, F);
+  uint16_t* dG = reinterpret_cast<uint16_t*>(p);
+  uint16_t* dU = reinterpret_cast<uint16_t*>(p + gated_hidden_bytes(M, F));
+  float* planes = reinterpret_cast<float*>(p + 2 * gated_hidden_bytes(M, F));
+  const int ldg = pad32(F);
+  GatedOperands o;
+  if (gated_operands(X, M, K, ldx, Wg, Wu, ldw, F, ws, o, st) != hipSuccess) return W4A4_ERR_HIP;
 
   GemmArgs g{};   // both projections again, then dG and dU rounded to bf16, the operands of what follows
-  g.A[0] = X, g.B[0] = Wg, g.B[1] = Wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
-  g.lda = ldx, g.ldb = ldw, g.ldo = F, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
+  g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
+  g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldg, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
   g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
   if ((act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_SILU>(g, st)
                             : launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_GELU>(g, st)) != hipSuccess)
     return W4A4_ERR_HIP;
 
   GemmArgs x{};   // dX = [dG dU] [Wg; Wu]
-  x.A[0] = dG, x.A[1] = dU, x.B[0] = Wg, x.B[1] = Wu;
-  x.lda = F, x.ldb = ldw, x.ldo = K, x.rows = M, x.cols = K, x.K = F;
+  x.A[0] = dG, x.A[1] = dU, x.B[0] = o.wg, x.B[1] = o.wu;
+  x.lda = ldg, x.ldb = o.ldw, x.ldo = K, x.rows = M, x.cols = K, x.K = F;
   x.segs = 2, x.probs = 1, x.steps = tiles_of(F, KSTEP), x.splits = gated_dx_splits(M, K, F);
   x.out[0] = x.splits > 1 ? static_cast<void*>(planes) : dX;
   if ((x.splits > 1 ? launch<ROWS, COLS, OUT_F32>(x, st) : launch<ROWS, COLS, OUT_BF16>(x, st)) != hipSuccess) return W4A4_ERR_HIP;
   if (x.splits > 1 && join(planes, x.splits, (long long)M * K, dX, st) != hipSuccess) return W4A4_ERR_HIP;
 
   GemmArgs w{};   // dWg = dG^T X, dWu = dU^T X
-  w.A[0] = dG, w.A[1] = dU, w.B[0] = X, w.out[0] = dWg, w.out[1] = dWu;
-  w.lda = F, w.ldb = ldx, w.ldo = K, w.rows = F, w.cols = K, w.K = M;
+  w.A[0] = dG, w.A[1] = dU, w.B[0] = o.x, w.out[0] = dWg, w.out[1] = dWu;
+  w.lda = ldg, w.ldb = o.ldx, w.ldo = K, w.rows = F, w.cols = K, w.K = M;
   w.segs = 1, w.probs = 2, w.splits = gated_dw_splits(M, K, F), w.steps = tiles_of(M, KSTEP);
   if (w.splits == 1) return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
   const long long n = (long long)F * K;
