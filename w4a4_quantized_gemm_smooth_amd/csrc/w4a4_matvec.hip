@@ -20,7 +20,8 @@
 // Work split: a block of 8 waves takes 8 or 16 tiles of W and a slice of K; x^ of the slice is made once a
 // block, in LDS; a wave takes one or two tiles and issues all its loads of codes before that. The down
 // projection t runs in blocks of its own beside those, 16 ranks and 2048 of K each. A second kernel adds
-// the slices in slice order, t L2 and the bias.
+// the slices in slice order, t L2 and the bias. Small layers (K <= 1024, L1 of at most 64 KB) are one kernel:
+// a block takes all of K, makes t for itself and finishes its rows.
 #include "w4a4_device_common.h"
 
 using namespace w4a4;
@@ -35,6 +36,9 @@ constexpr int MV_TK = 2048;      // K of a block of the down projection: 256 a w
 #define W4A4_MV_TARGET 256
 #endif
 
+constexpr int MV_SMALL_K = 1024, MV_SMALL_L1 = 32768;   // one kernel up to this K and K * rank_pad
+
+inline bool mv_small(int K, int rp) { return K <= MV_SMALL_K && K * rp <= MV_SMALL_L1; }
 inline int mv_tiles(int N) { return (N + 15) / 16; }
 inline int mv_pairs(int K) { return (K + 2 * W4A4_GROUP - 1) / (2 * W4A4_GROUP); }
 inline int mv_tslices(int K) { return (K + MV_TK - 1) / MV_TK; }
@@ -195,48 +199,42 @@ __device__ __forceinline__ void down_block(const uint16_t* __restrict__ X, int l
   }
 }
 
-// TWO: M > 8, the hi and lo rows are two operands. Blocks 0 .. tb - 1: the down projection; then slice by
-// slice the rows of W.
-template <bool MX, bool TWO, int NT, int SP>
-__global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __restrict__ X, int ldx,
-                                                            const float* __restrict__ inv, const uint16_t* __restrict__ l1t,
-                                                            const uint8_t* __restrict__ wv, int M, int N, int K, int rp,
-                                                            int nb, int tb, float* __restrict__ part,
-                                                            float* __restrict__ tpart) {
-  constexpr int STRIDE = SP * 256 + 64;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  float* sums = reinterpret_cast<float*>(lds);
-  uint8_t* xs = lds + 2 * SP * 16 * 4;
-  if ((int)blockIdx.x < tb) {
-    down_block<TWO>(X, ldx, inv, l1t, M, K, rp, blockIdx.x % (rp / 16), blockIdx.x / (rp / 16), sums, tpart);
-    return;
-  }
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
-  const int slice = (blockIdx.x - tb) / nb, b = (blockIdx.x - tb) % nb;
-  const int P = (K / W4A4_GROUP + 1) / 2, tiles = (N + 15) / 16, p0 = slice * SP, np = min(SP, P - p0);
-  const int tile0 = (b * MV_WAVES + wave) * NT;
+// A wave's codes and scales of NT tiles and SP pairs, all on their way at once; tiles and pairs past the end
+// repeat the last one, unused.
+template <int NT, int SP>
+struct Codes {
   v4i w[NT][SP];
   uint32_t sc[NT][SP];
+  __device__ __forceinline__ void load(const uint8_t* __restrict__ wv, int tile0, int tiles, int P, int p0, int np, int lane) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {   // tiles and pairs past the end repeat the last one, unused
-    const size_t at = (size_t)min(tile0 + n, tiles - 1) * P + p0;
-    const v4i* cw = reinterpret_cast<const v4i*>(wv) + at * 64 + lane;
-    const uint32_t* sw = reinterpret_cast<const uint32_t*>(wv + (size_t)tiles * P * 1024) + at * 16 + r;
+    for (int n = 0; n < NT; ++n) {
+      const size_t at = (size_t)min(tile0 + n, tiles - 1) * P + p0;
+      const v4i* cw = reinterpret_cast<const v4i*>(wv) + at * 64 + lane;
+      const uint32_t* sw = reinterpret_cast<const uint32_t*>(wv + (size_t)tiles * P * 1024) + at * 16 + (lane & 15);
 #pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      const int q = min(i, np - 1);
-      w[n][i] = cw[q * 64];
-      sc[n][i] = sw[q * 16];
+      for (int i = 0; i < SP; ++i) {
+        const int q = min(i, np - 1);
+        w[n][i] = cw[q * 64];
+        sc[n][i] = sw[q * 16];
+      }
     }
   }
-  stage_x<SP, TWO, !MX>(X, ldx, inv, M, K, p0 * 128, xs, sums);
-  if (tile0 >= tiles) return;
-  const int row_hi = TWO ? (r < M ? r : 2 * M) : (r < 8 ? (r < M ? r : 2 * M) : (r - 8 < M ? M + r - 8 : 2 * M));
-  const uint8_t* xh = xs + row_hi * STRIDE + 16 * j;
+};
+
+// The row of the staged x^ (hi part, or the only operand) that lane row r reads
+template <bool TWO>
+__device__ __forceinline__ int x_row(int r, int M) {
+  return TWO ? (r < M ? r : 2 * M) : (r < 8 ? (r < M ? r : 2 * M) : (r - 8 < M ? M + r - 8 : 2 * M));
+}
+
+// acc += codes times x^ over np pairs
+template <bool MX, bool TWO, int NT, int SP>
+__device__ __forceinline__ void accumulate(const Codes<NT, SP>& c, const uint8_t* xs, const float* sums, int M, int np, int lane,
+                                           v4f (&acc)[NT]) {
+  constexpr int STRIDE = SP * 256 + 64;
+  const int r = lane & 15, j = lane >> 4;
+  const uint8_t* xh = xs + x_row<TWO>(r, M) * STRIDE + 16 * j;
   const uint8_t* xl = xs + (r < M ? M + r : 2 * M) * STRIDE + 16 * j;   // TWO only
-  v4f acc[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < SP; ++i) {
     if (i >= np) break;
@@ -249,30 +247,59 @@ __global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __re
       if (!MX && (d & 1) == 0) start = *reinterpret_cast<const v4f*>(sums + (2 * i + (d >> 1)) * 16 + 4 * j);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t c = (uint32_t)w[n][i][d];
+        const uint32_t w = (uint32_t)c.w[n][i][d];
         v4i op;
         if constexpr (MX) {
-          op[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
-          op[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 1));
-          op[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 2));
-          op[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 3));
+          op[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+          op[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+          op[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+          op[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
         } else {
-          op[0] = (int)(((c << 3) & 0x00780078u) | 0x41804180u);
-          op[1] = (int)(((c >> 1) & 0x00780078u) | 0x41804180u);
-          op[2] = (int)(((c >> 5) & 0x00780078u) | 0x41804180u);
-          op[3] = (int)(((c >> 9) & 0x00780078u) | 0x41804180u);
+          op[0] = (int)(((w << 3) & 0x00780078u) | 0x41804180u);
+          op[1] = (int)(((w >> 1) & 0x00780078u) | 0x41804180u);
+          op[2] = (int)(((w >> 5) & 0x00780078u) | 0x41804180u);
+          op[3] = (int)(((w >> 9) & 0x00780078u) | 0x41804180u);
         }
         pt[n] = mfma16(h, op, MX || (d & 1) == 0 ? start : pt[n]);
         if (TWO) pt[n] = mfma16(l, op, pt[n]);
         if (MX || (d & 1)) {
-          const float s = MX ? e8m0((sc[n][i] >> (8 * d)) & 255u)
-                             : (d == 1 ? __uint_as_float(sc[n][i] << 16) : __uint_as_float(sc[n][i] & 0xFFFF0000u));
+          const uint32_t sc = c.sc[n][i];
+          const float s = MX ? e8m0((sc >> (8 * d)) & 255u) : (d == 1 ? __uint_as_float(sc << 16) : __uint_as_float(sc & 0xFFFF0000u));
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[n][v] = fmaf(s, pt[n][v], acc[n][v]);
         }
       }
     }
   }
+}
+
+// TWO: M > 8, the hi and lo rows are two operands. Blocks 0 .. tb - 1: the down projection; then slice by
+// slice the rows of W.
+template <bool MX, bool TWO, int NT, int SP>
+__global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __restrict__ X, int ldx,
+                                                            const float* __restrict__ inv, const uint16_t* __restrict__ l1t,
+                                                            const uint8_t* __restrict__ wv, int M, int N, int K, int rp,
+                                                            int nb, int tb, float* __restrict__ part,
+                                                            float* __restrict__ tpart) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* sums = reinterpret_cast<float*>(lds);
+  uint8_t* xs = lds + 2 * SP * 16 * 4;
+  if ((int)blockIdx.x < tb) {
+    down_block<TWO>(X, ldx, inv, l1t, M, K, rp, blockIdx.x % (rp / 16), blockIdx.x / (rp / 16), sums, tpart);
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
+  const int slice = (blockIdx.x - tb) / nb, b = (blockIdx.x - tb) % nb;
+  const int P = (K / W4A4_GROUP + 1) / 2, tiles = (N + 15) / 16, p0 = slice * SP, np = min(SP, P - p0);
+  const int tile0 = (b * MV_WAVES + wave) * NT;
+  Codes<NT, SP> codes;
+  codes.load(wv, tile0, tiles, P, p0, np, lane);
+  stage_x<SP, TWO, !MX>(X, ldx, inv, M, K, p0 * 128, xs, sums);
+  if (tile0 >= tiles) return;
+  v4f acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
+  accumulate<MX, TWO, NT, SP>(codes, xs, sums, M, np, lane, acc);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (tile0 + n >= tiles) break;
@@ -287,6 +314,87 @@ __global__ __launch_bounds__(MV_THREADS) void matvec_kernel(const uint16_t* __re
       if (m < M && (TWO || j < 2)) out[(size_t)m * (tiles * 16)] = acc[n][v];
     }
   }
+}
+
+// The layer in one kernel (K <= 128 SP): a block takes 8 tiles of W and all of K. Its waves share the ranks'
+// 16-row tiles and the pairs of the down projection; t then goes to the matrix unit as x^ does, hi and lo,
+// and t L2 accumulates onto the codes' sums.
+template <bool MX, bool TWO, int SP>
+__global__ __launch_bounds__(MV_THREADS) void matvec_small_kernel(const uint16_t* __restrict__ X, int ldx,
+                                                                  const float* __restrict__ inv,
+                                                                  const uint16_t* __restrict__ l1t,
+                                                                  const uint8_t* __restrict__ wv,
+                                                                  const uint16_t* __restrict__ l2t,
+                                                                  const uint16_t* __restrict__ bias, int M, int N, int K,
+                                                                  int rp, uint16_t* __restrict__ Y, int ldy) {
+  constexpr int STRIDE = SP * 256 + 64, TSTRIDE = W4A4_MAX_RANK * 2 + 16;   // t rows: 16 bytes x an odd number, other banks
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* sums = reinterpret_cast<float*>(lds);
+  uint8_t* xs = lds + 2 * SP * 16 * 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, j = lane >> 4;
+  const int P = (K / W4A4_GROUP + 1) / 2, tiles = (N + 15) / 16, tile = blockIdx.x * MV_WAVES + wave;
+  Codes<1, SP> codes;
+  codes.load(wv, tile, tiles, P, 0, P, lane);
+  stage_x<SP, TWO, !MX>(X, ldx, inv, M, K, 0, xs, sums);
+  v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
+  accumulate<MX, TWO, 1, SP>(codes, xs, sums, M, P, lane, acc);
+  if (rp > 0) {
+    const int rt = rp / 16, nsub = MV_WAVES / rt, rtile = wave % rt, sub = wave / rt;
+    const uint8_t* xh = xs + x_row<TWO>(r, M) * STRIDE + 16 * j;
+    const uint8_t* xl = xs + (r < M ? M + r : 2 * M) * STRIDE + 16 * j;   // TWO only
+    const uint16_t* l = l1t + (size_t)(rtile * 16 + r) * K + 8 * j;
+    v4f t = {0.f, 0.f, 0.f, 0.f};
+    if (sub < nsub)
+      for (int i = sub; i < P; i += nsub)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const v4i w = i * 128 + 32 * d < K ? *reinterpret_cast<const v4i*>(l + i * 128 + 32 * d) : v4i{0, 0, 0, 0};
+          t = mfma16(*reinterpret_cast<const v4i*>(xh + i * 256 + 64 * d), w, t);
+          if (TWO) t = mfma16(*reinterpret_cast<const v4i*>(xl + i * 256 + 64 * d), w, t);
+        }
+    if (!TWO) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) t[v] += __shfl_xor(t[v], 32);
+    }
+    __syncthreads();   // x^ is done with
+    float* red = reinterpret_cast<float*>(xs);                 // [waves][16][16]
+    uint8_t* ts = xs + MV_WAVES * 1024;                        // t as operand rows: TWO hi 0..15, lo 16..31; else hi 0..7, lo 8..15
+#pragma unroll
+    for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * j + v) * 16 + r] = t[v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < (TWO ? 16 : 8) * rp; i += MV_THREADS) {
+      const int m = i / rp, c = i % rp;
+      float s = 0.f;
+      if (m < M)
+        for (int q = 0; q < nsub; ++q) s += red[((q * rt + (c >> 4)) * 16 + m) * 16 + (c & 15)];
+      const uint32_t hi = pack_bf16x2(s, 0.f);
+      const uint32_t lo = pack_bf16x2(s - __uint_as_float(hi << 16), 0.f);
+      *reinterpret_cast<uint16_t*>(ts + m * TSTRIDE + 2 * c) = (uint16_t)hi;
+      *reinterpret_cast<uint16_t*>(ts + (m + (TWO ? 16 : 8)) * TSTRIDE + 2 * c) = (uint16_t)lo;
+    }
+    __syncthreads();
+    const uint16_t* l2 = l2t + (size_t)min(tile * 16 + r, N - 1) * rp;
+    for (int c = 8 * j; c - 8 * j < rp; c += 32) {   // 32 ranks an operand, the last half empty where rp is odd in 16
+      const bool in = c < rp;
+      const v4i w = in ? *reinterpret_cast<const v4i*>(l2 + c) : v4i{0, 0, 0, 0};
+      const v4i h = in ? *reinterpret_cast<const v4i*>(ts + r * TSTRIDE + 2 * c) : v4i{0, 0, 0, 0};
+      acc[0] = mfma16(h, w, acc[0]);
+      if (TWO) {
+        const v4i lo = in ? *reinterpret_cast<const v4i*>(ts + (16 + r) * TSTRIDE + 2 * c) : v4i{0, 0, 0, 0};
+        acc[0] = mfma16(lo, w, acc[0]);
+      }
+    }
+  }
+  if (!TWO) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[0][v] += __shfl_xor(acc[0][v], 32);
+  }
+  const int n = tile * 16 + r;
+  if (n >= N || (!TWO && j >= 2)) return;
+  const float bb = bias ? bf16f(bias[n]) : 0.f;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (4 * j + v < M) Y[(size_t)(4 * j + v) * ldy + n] = (uint16_t)pack_bf16x2(acc[0][v] + bb, 0.f);
 }
 
 // y = the slices' sums + t L2 + bias. A block takes one row and 128 columns: 32 threads four columns each,
@@ -375,6 +483,30 @@ hipError_t dispatch(int sp, const MatvecArgs& a, hipStream_t st) {
   }
 }
 
+template <bool MX, bool TWO, int SP>
+hipError_t launch_small(const MatvecArgs& a, const uint16_t* l2t, const uint16_t* bias, uint16_t* Y, int ldy, hipStream_t st) {
+  size_t lds = (size_t)(2 * a.M + 1) * (SP * 256 + 64);
+  const size_t t = MV_WAVES * 1024 + (TWO ? 32 : 16) * (W4A4_MAX_RANK * 2 + 16);   // the down projection's sums and t
+  lds = 2 * SP * 16 * 4 + (lds > t ? lds : t);
+  if (lds > 65536) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&matvec_small_kernel<MX, TWO, SP>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+    if (attr != hipSuccess) return attr;
+  }
+  hipLaunchKernelGGL((matvec_small_kernel<MX, TWO, SP>), dim3((mv_tiles(a.N) + MV_WAVES - 1) / MV_WAVES), dim3(MV_THREADS), lds, st, a.X,
+                     a.ldx, a.inv, a.l1t, a.wv, l2t, bias, a.M, a.N, a.K, a.rp, Y, ldy);
+  return hipGetLastError();
+}
+
+template <bool MX, bool TWO>
+hipError_t dispatch_small(const MatvecArgs& a, const uint16_t* l2t, const uint16_t* bias, uint16_t* Y, int ldy, hipStream_t st) {
+  const int P = mv_pairs(a.K);
+  if (P <= 1) return launch_small<MX, TWO, 1>(a, l2t, bias, Y, ldy, st);
+  if (P <= 2) return launch_small<MX, TWO, 2>(a, l2t, bias, Y, ldy, st);
+  if (P <= 4) return launch_small<MX, TWO, 4>(a, l2t, bias, Y, ldy, st);
+  return launch_small<MX, TWO, 8>(a, l2t, bias, Y, ldy, st);
+}
+
 template <bool MX>
 hipError_t dispatch(int sp, const MatvecArgs& a, hipStream_t st) {
   if (a.M <= 8) return dispatch<MX, false, 1>(sp, a, st);
@@ -398,7 +530,7 @@ w4a4_status_t w4a4_matvec_sizes(int M, int N, int K, int rank, int fmt, size_t* 
   if (!wv || !ws) return W4A4_ERR_INVALID_ARG;
   const size_t P = mv_pairs(K), tiles = mv_tiles(N), sp = mv_slice(M, N, K), slices = (P + sp - 1) / sp;
   *wv = tiles * P * (1024 + 64);
-  *ws = M * (slices * tiles * 16 + (size_t)mv_tslices(K) * rank_pad_of(rank)) * sizeof(float);
+  *ws = mv_small(K, rank_pad_of(rank)) ? 64 : M * (slices * tiles * 16 + (size_t)mv_tslices(K) * rank_pad_of(rank)) * sizeof(float);
   return W4A4_OK;
 }
 
@@ -428,7 +560,13 @@ w4a4_status_t w4a4_matvec(const uint16_t* X, int M, int K, int ldx, const float*
   float* tpart = part + (size_t)slices * M * (mv_tiles(N) * 16);
   const MatvecArgs a{X, ldx, inv_lambda, l1t, wv, M, N, K, rp, part, tpart};
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const hipError_t e = fmt == W4A4_FMT_MXFP4_B32 ? dispatch<true>(sp, a, st) : dispatch<false>(sp, a, st);
+  const bool mx = fmt == W4A4_FMT_MXFP4_B32;
+  if (mv_small(K, rp)) {
+    const hipError_t e = M <= 8 ? (mx ? dispatch_small<true, false>(a, l2t, bias, Y, ldy, st) : dispatch_small<false, false>(a, l2t, bias, Y, ldy, st))
+                                : (mx ? dispatch_small<true, true>(a, l2t, bias, Y, ldy, st) : dispatch_small<false, true>(a, l2t, bias, Y, ldy, st));
+    return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+  }
+  const hipError_t e = mx ? dispatch<true>(sp, a, st) : dispatch<false>(sp, a, st);
   if (e != hipSuccess) return W4A4_ERR_HIP;
   hipLaunchKernelGGL(matvec_finish_kernel, dim3((N + 127) / 128, M), dim3(256), 0, st, part, slices, tpart, mv_tslices(K), l2t, bias, M,
                      N, rp, Y, ldy);
