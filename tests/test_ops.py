@@ -597,6 +597,66 @@ def test_gradients_against_differences(op):
         assert abs(got - want) <= rel * 4 * scale + 1e-6 * abs(want), (i, got, want)
 
 
+# ------------------------------------------------------------------- offsets beyond 32 bits
+def _big(M, K, seed):
+    """[M, K] bf16 of more than 2^31 elements: one random stretch of 4096 rows after another, shifted."""
+    base = _rand(seed, (4096, K))
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, M, 4096):
+        n = min(4096, M - i)
+        x[i: i + n] = torch.roll(base, i // 4096, 0)[:n]
+    return x
+
+
+@gpu
+def test_layer_norm_beyond_32_bits():
+    M, K = 1_050_001, 2050
+    c = dict(M=M, K=K, x=_big(M, K, 1), gamma=_rand(2, (K,)), beta=_rand(3, (K,)))
+    y, mean, rstd = _norm_forward(c)
+    dx = torch.empty_like(y)
+    w4.layer_norm_backward(c["x"], c["x"], c["gamma"], mean, rstd, dx, None, None, None)
+    rows = torch.tensor([0, 1, 524_287, 1_047_000, M - 2, M - 1])
+    s = dict(c, M=len(rows), x=c["x"][rows.cuda()], dy=c["x"][rows.cuda()])
+    _check_norm_forward(s, y[rows.cuda()], mean[rows.cuda()], rstd[rows.cuda()])
+    _check_norm_backward(s, mean[rows.cuda()], rstd[rows.cuda()], dx[rows.cuda()], None, None)
+
+
+@gpu
+def test_checkpoint_beyond_32_bits():
+    M, K = 1_060_000, 2056
+    x = _big(M, K, 4)
+    codes, scales = _pack(x)
+    back = torch.empty_like(x)
+    w4.checkpoint_unpack(codes, scales, back)
+    for r in (0, 512_000, M - 64):
+        q, e, want = _pack64(x[r: r + 64])
+        b = r // 32
+        assert torch.equal(codes[b: b + 2].cpu(), q) and torch.equal(scales[b: b + 2].cpu(), e)
+        assert torch.equal(back[r: r + 64].cpu().double(), want)
+    del back
+    # one token of the last block and one of the first reach the gradient: whole numbers, exact
+    dy = torch.zeros((M, 264), dtype=torch.bfloat16, device="cuda")
+    dy[M - 1, 5], dy[3, 7] = 1.0, 2.0
+    for n in (264, 8):
+        dw = torch.empty((n, K), device="cuda")
+        w4.checkpoint_weight_grad(dy[:, :n], codes, scales, K, dw, _empty(w4.checkpoint_weight_grad_bytes(M, n, K)))
+        want = torch.zeros((n, K), dtype=torch.float64)
+        want[5], want[7] = _pack64(x[M - 32:])[2][31], 2 * _pack64(x[:32])[2][3]
+        assert torch.equal(dw.cpu().double(), want), n
+
+
+@gpu
+def test_gated_beyond_32_bits():
+    M, K, F = 66_001, 64, 32_776
+    x, wg, wu = _rand(1, (M, K)), _rand(2, (F, K), 0.125), _rand(3, (F, K), 0.125)
+    h = torch.full((M, F), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.gated_forward(x, wg, wu, "silu", h, _empty(w4.gated_forward_bytes(M, K, F)))
+    rows = torch.tensor([0, 40_000, 65_535, 65_536, M - 1])
+    r = _gated64(x[rows.cuda()].cpu().double(), wg.cpu().double(), wu.cpu().double(), "silu")
+    _within(h[rows.cuda()].cpu(), r["h"], r["eh"] + U16 * (r["h"].abs() + r["eh"]) + 1e-30, "h")
+    assert not torch.isnan(h).any()   # every element is written
+
+
 # ----------------------------------------------------------------------------- streams and graphs
 def _all_ops():
     """Calls of every operator on fixed inputs, as (call, outputs)."""
