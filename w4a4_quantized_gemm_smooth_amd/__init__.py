@@ -435,17 +435,26 @@ def _matrix(name, t):
         dev = t.device
     except (AttributeError, ValueError):
         raise ValueError(f"{name} must be a 2-D tensor") from None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU (got {dev})")
     now = (_torch or lib() and _torch)._C._cuda_getDevice()
-    if dev.index != now:
+    if dev.index != now:   # (None for the CPU)
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a GPU (got {dev})")
         raise ValueError(f"{name} is on {dev}, the current device is cuda:{now}")
     return M, K, dev
 
 
-def _ld(t):
-    """Row stride of a matrix; torch leaves the stride of a single row free, then its width."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(name, t, dtype, shape, device):
+    """Row stride of a matrix of a given type and shape whose rows are contiguous and do not overlap (torch
+    leaves the stride of a single row free: then its width)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device:
+            s0, s1 = t.stride()
+            if s1 == 1 and s0 >= shape[1]:
+                return s0 if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass
+    _check_tensor(name, t, dtype, shape, device, False)
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _ptr(t):
@@ -497,19 +506,20 @@ def matvec(x, inv_lambda, l1t, wv, l2t, bias, y, N, K, rank, fmt, ws, stream=Non
     f = _fmt(fmt)
     M, _, dev = _matrix("x", x)
     wv_bytes, ws_bytes = _two_sizes("w4a4_matvec_sizes", M, N, K, rank, f)
-    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
-    _check_tensor("y", y, _torch.bfloat16, (M, N), dev, False)
+    ldx = _rows("x", x, _torch.bfloat16, (M, K), dev)
+    ldy = _rows("y", y, _torch.bfloat16, (M, N), dev)
     rp = (rank + RANK_ALIGN - 1) // RANK_ALIGN * RANK_ALIGN
     _check_bytes("inv_lambda", inv_lambda, 4 * K, dev)
     _check_bytes("wv", wv, wv_bytes, dev)
     _check_bytes("ws", ws, ws_bytes, dev)
-    _check_bytes("l1t", l1t, 2 * rp * K, dev)
-    _check_bytes("l2t", l2t, 2 * rp * N, dev)
+    if rp:
+        _check_bytes("l1t", l1t, 2 * rp * K, dev)
+        _check_bytes("l2t", l2t, 2 * rp * N, dev)
     if bias is not None:
         _check_bytes("bias", bias, 2 * N, dev)
     st = _lib.w4a4_matvec(
-        _ptr(x), M, K, _ld(x), _ptr(inv_lambda), _ptr(l1t), _ptr(wv), _ptr(l2t), _ptr(bias), _ptr(y), _ld(y), N, rank, f,
-        _ptr(ws), _queue(stream, dev))
+        x.data_ptr(), M, K, ldx, inv_lambda.data_ptr(), _ptr(l1t), wv.data_ptr(), _ptr(l2t), _ptr(bias), y.data_ptr(), ldy, N,
+        rank, f, ws.data_ptr(), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_matvec", st)
 
@@ -522,27 +532,22 @@ def _dtype(t, name):
     return 1
 
 
-def _norm_params(gamma, beta, K, dev):
-    p = gamma if gamma is not None else beta
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _check_tensor(name, t, p.dtype, (K,), dev)
-    return _dtype(p, "gamma and beta")
-
-
 def layer_norm(x, gamma, beta, eps, y, mean, rstd, stream=None):
     """y = (x - mean) rstd gamma + beta over the rows of x [M, K] (bf16 or fp32; gamma, beta [K] bf16, fp32
     or None), with the rows' mean and rstd [M] fp32 for ``layer_norm_backward``."""
     M, K, dev = _matrix("x", x)
-    dt = _dtype(x, "x")
-    _check_tensor("x", x, x.dtype, (M, K), dev, False)
-    _check_tensor("y", y, x.dtype, (M, K), dev, False)
-    _check_tensor("mean", mean, _torch.float32, (M,), dev)
-    _check_tensor("rstd", rstd, _torch.float32, (M,), dev)
-    pt = _norm_params(gamma, beta, K, dev)
+    dtype, f32 = x.dtype, _torch.float32
+    ldx, ldy = _rows("x", x, dtype, (M, K), dev), _rows("y", y, dtype, (M, K), dev)
+    _check_tensor("mean", mean, f32, (M,), dev)
+    _check_tensor("rstd", rstd, f32, (M,), dev)
+    p = gamma if gamma is not None else beta
+    if gamma is not None:
+        _check_tensor("gamma", gamma, gamma.dtype, (K,), dev)
+    if beta is not None:
+        _check_tensor("beta", beta, p.dtype, (K,), dev)
     st = _lib.w4a4_layer_norm(
-        _ptr(x), M, K, _ld(x), dt, _ptr(gamma), _ptr(beta), pt, eps, _ptr(y), _ld(y), _ptr(mean), _ptr(rstd),
-        _queue(stream, dev))
+        x.data_ptr(), M, K, ldx, _dtype(x, "x"), _ptr(gamma), _ptr(beta), _dtype(p, "gamma and beta"), eps, y.data_ptr(), ldy,
+        mean.data_ptr(), rstd.data_ptr(), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_layer_norm", st)
 
@@ -555,19 +560,21 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=
     """dx, and dgamma, dbeta [K] fp32 (either may be None; ``ws`` may be None where both are), of
     ``layer_norm`` from dy, x and the forward pass's mean and rstd."""
     M, K, dev = _matrix("x", x)
-    dt = _dtype(x, "x")
-    for name, t in (("dy", dy), ("x", x), ("dx", dx)):
-        _check_tensor(name, t, x.dtype, (M, K), dev, False)
-    _check_tensor("mean", mean, _torch.float32, (M,), dev)
-    _check_tensor("rstd", rstd, _torch.float32, (M,), dev)
-    for name, t in (("dgamma", dgamma), ("dbeta", dbeta)):
-        if t is not None:
-            _check_tensor(name, t, _torch.float32, (K,), dev)
-    pt = _norm_params(gamma, None, K, dev)
-    _check_bytes("ws", ws, 0 if dgamma is None and dbeta is None else layer_norm_backward_bytes(M, K), dev)
+    dtype, shape, f32 = x.dtype, (M, K), _torch.float32
+    ldx, lddy, lddx = _rows("x", x, dtype, shape, dev), _rows("dy", dy, dtype, shape, dev), _rows("dx", dx, dtype, shape, dev)
+    _check_tensor("mean", mean, f32, (M,), dev)
+    _check_tensor("rstd", rstd, f32, (M,), dev)
+    if gamma is not None:
+        _check_tensor("gamma", gamma, gamma.dtype, (K,), dev)
+    if dgamma is not None:
+        _check_tensor("dgamma", dgamma, f32, (K,), dev)
+    if dbeta is not None:
+        _check_tensor("dbeta", dbeta, f32, (K,), dev)
+    if dgamma is not None or dbeta is not None:
+        _check_bytes("ws", ws, layer_norm_backward_bytes(M, K), dev)
     st = _lib.w4a4_layer_norm_backward(
-        _ptr(dy), _ld(dy), _ptr(x), _ld(x), dt, _ptr(gamma), pt, _ptr(mean), _ptr(rstd), M, K, _ptr(dx), _ld(dx),
-        _ptr(dgamma), _ptr(dbeta), _ptr(ws), _queue(stream, dev))
+        dy.data_ptr(), lddy, x.data_ptr(), ldx, _dtype(x, "x"), _ptr(gamma), _dtype(gamma, "gamma"), mean.data_ptr(),
+        rstd.data_ptr(), M, K, dx.data_ptr(), lddx, _ptr(dgamma), _ptr(dbeta), _ptr(ws), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_layer_norm_backward", st)
 
@@ -587,10 +594,10 @@ def _check_checkpoint(codes, scales, M, K, dev):
 def checkpoint_pack(x, codes, scales, stream=None):
     """Keep x [M, K] bf16 in 8 bits: int8 codes and a power-of-two scale per channel and 32 tokens."""
     M, K, dev = _matrix("x", x)
-    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
+    ldx = _rows("x", x, _torch.bfloat16, (M, K), dev)
     _check_checkpoint(codes, scales, M, K, dev)
     st = _lib.w4a4_checkpoint_pack(
-        _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _queue(stream, dev))
+        x.data_ptr(), M, K, ldx, codes.data_ptr(), scales.data_ptr(), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_checkpoint_pack", st)
 
@@ -598,10 +605,10 @@ def checkpoint_pack(x, codes, scales, stream=None):
 def checkpoint_unpack(codes, scales, x, stream=None):
     """What the codes and scales stand for, into x [M, K] bf16 (exact)."""
     M, K, dev = _matrix("x", x)
-    _check_tensor("x", x, _torch.bfloat16, (M, K), dev, False)
+    ldx = _rows("x", x, _torch.bfloat16, (M, K), dev)
     _check_checkpoint(codes, scales, M, K, dev)
     st = _lib.w4a4_checkpoint_unpack(
-        _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x), _queue(stream, dev))
+        codes.data_ptr(), scales.data_ptr(), M, K, x.data_ptr(), ldx, _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_checkpoint_unpack", st)
 
@@ -614,13 +621,13 @@ def checkpoint_weight_grad(dy, codes, scales, K, dw, ws, stream=None):
     """dw [N, K] (fp32 or bf16) = dy^T x for dy [M, N] bf16 and the activations [M, K] kept in (codes,
     scales)."""
     M, N, dev = _matrix("dy", dy)
-    _check_tensor("dy", dy, _torch.bfloat16, (M, N), dev, False)
+    lddy = _rows("dy", dy, _torch.bfloat16, (M, N), dev)
     _check_checkpoint(codes, scales, M, K, dev)
     dt = _dtype(dw, "dw")
     _check_tensor("dw", dw, dw.dtype, (N, K), dev)
     _check_bytes("ws", ws, checkpoint_weight_grad_bytes(M, N, K), dev)
     st = _lib.w4a4_checkpoint_weight_grad(
-        _ptr(dy), _ld(dy), _ptr(codes), _ptr(scales), M, N, K, _ptr(dw), dt, _ptr(ws), _queue(stream, dev))
+        dy.data_ptr(), lddy, codes.data_ptr(), scales.data_ptr(), M, N, K, dw.data_ptr(), dt, ws.data_ptr(), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_checkpoint_weight_grad", st)
 
@@ -635,13 +642,10 @@ def _check_gated(x, wg, wu, h, name):
     M, K, dev = _matrix("x", x)
     F = _matrix("wg", wg)[0]
     bf16 = _torch.bfloat16
-    _check_tensor("x", x, bf16, (M, K), dev, False)
-    _check_tensor("wg", wg, bf16, (F, K), dev, False)
-    _check_tensor("wu", wu, bf16, (F, K), dev, False)
-    _check_tensor(name, h, bf16, (M, F), dev, False)
-    if _ld(wg) != _ld(wu):
+    ldx, ldw = _rows("x", x, bf16, (M, K), dev), _rows("wg", wg, bf16, (F, K), dev)
+    if _rows("wu", wu, bf16, (F, K), dev) != ldw:
         raise ValueError("wg and wu must have the same row stride")
-    return M, K, F, dev
+    return M, K, F, dev, ldx, ldw, _rows(name, h, bf16, (M, F), dev)
 
 
 def gated_forward_bytes(M: int, K: int, F: int) -> int:
@@ -650,10 +654,10 @@ def gated_forward_bytes(M: int, K: int, F: int) -> int:
 
 def gated_forward(x, wg, wu, act, h, ws=None, stream=None):
     """h [M, F] = act(x wg^T) * (x wu^T) for x [M, K], wg and wu [F, K], bf16; act "silu" or "gelu"."""
-    M, K, F, dev = _check_gated(x, wg, wu, h, "h")
+    M, K, F, dev, ldx, ldw, ldh = _check_gated(x, wg, wu, h, "h")
     _check_bytes("ws", ws, gated_forward_bytes(M, K, F), dev)
     st = _lib.w4a4_gated_forward(
-        _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(h), _ld(h), _ptr(ws), _queue(stream, dev))
+        x.data_ptr(), M, K, ldx, wg.data_ptr(), wu.data_ptr(), ldw, F, _act(act), h.data_ptr(), ldh, _ptr(ws), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_gated_forward", st)
 
@@ -664,13 +668,13 @@ def gated_backward_bytes(M: int, K: int, F: int) -> int:
 
 def gated_backward(dh, x, wg, wu, act, dx, dwg, dwu, ws, stream=None):
     """dx [M, K], dwg and dwu [F, K] (bf16) of ``gated_forward`` from dh [M, F] and its inputs."""
-    M, K, F, dev = _check_gated(x, wg, wu, dh, "dh")
+    M, K, F, dev, ldx, ldw, lddh = _check_gated(x, wg, wu, dh, "dh")
     for n, t, shape in (("dx", dx, (M, K)), ("dwg", dwg, (F, K)), ("dwu", dwu, (F, K))):
         _check_tensor(n, t, _torch.bfloat16, shape, dev)
     _check_bytes("ws", ws, gated_backward_bytes(M, K, F), dev)
     st = _lib.w4a4_gated_backward(
-        _ptr(dh), _ld(dh), _ptr(x), M, K, _ld(x), _ptr(wg), _ptr(wu), _ld(wg), F, _act(act), _ptr(dx), _ptr(dwg),
-        _ptr(dwu), _ptr(ws), _queue(stream, dev))
+        dh.data_ptr(), lddh, x.data_ptr(), M, K, ldx, wg.data_ptr(), wu.data_ptr(), ldw, F, _act(act), dx.data_ptr(),
+        dwg.data_ptr(), dwu.data_ptr(), ws.data_ptr(), _queue(stream, dev))
     if st:
         raise W4A4Error("w4a4_gated_backward", st)
 
