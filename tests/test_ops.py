@@ -119,7 +119,8 @@ def _matvec_reference(c, x=None):
     (1, 1, 64, 0, False), (1, 17, 64, 1, True), (2, 128, 128, 16, False), (7, 129, 192, 20, True), (8, 300, 1088, 48, True),
     (9, 64, 320, 0, True), (16, 255, 2048, 128, True), (13, 640, 8256, 33, False), (1, 9216, 1024, 32, False),
     (16, 20000, 64, 16, True), (5, 40, 12288, 20, True),
-    (16, 100, 960, 33, True), (12, 77, 512, 64, False), (3, 150, 1024, 128, True), (8, 1000, 1024, 17, True), (10, 500, 448, 0, False)])
+    (16, 100, 960, 33, True), (12, 77, 512, 64, False), (3, 150, 1024, 128, True), (8, 1000, 1024, 17, True), (10, 500, 448, 0, False),
+    (8, 333, 2048, 32, True), (1, 700, 1984, 20, False), (5, 260, 1152, 48, True)])
 def test_matvec(fmt, M, N, K, rank, bias):
     c = _matvec_case(M, N, K, rank, fmt, bias, seed=M + N + K)
     y, tol = _matvec_reference(c)

@@ -13,7 +13,9 @@
 //
 // Both kernels move each byte once and are bound by that; a thread owns 4 channels of a block: 32 loads
 // (or stores) of 8 bytes down the tokens, one 128-byte line of codes. Packing passes the lines through LDS,
-// so that a wave stores whole KBs instead of 16 bytes of 64 lines at a time (4608 x 12288: 47 us without).
+// so that a wave stores whole KBs instead of 16 bytes of 64 lines at a time. 4608 x 12288: packing 38.6 us
+// (4.4 TB/s; 47 us without the lines), reading back 25.5 us (6.7 TB/s, in part from the memory-side cache; a
+// large copy moves 4.9 TB/s).
 #include "w4a4_device_common.h"
 
 using namespace w4a4;

