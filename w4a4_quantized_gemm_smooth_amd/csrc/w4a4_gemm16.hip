@@ -21,8 +21,8 @@
 //   CODES  8-bit codes with a scale per column and step (B only): 32 bytes of contraction to a column,
 //          converted after the read; the values are bf16 numbers, so nothing is rounded.
 // Outside its range a copy's address is moved past the buffer's end, which reads as zero, so ragged
-// sizes cost nothing in the loop. bf16 results are computed transposed (B as the first operand), which
-// leaves a lane four neighbouring columns of a row.
+// sizes cost nothing in the loop. Results are computed transposed (B as the first operand), which leaves a
+// lane four neighbouring columns of a row.
 //
 // Measured: gated forward 4608 x 4096 x 12288 787 us = 1180 TFLOP/s (the library's product of the same size
 // 1084, its 8192^3 1290), at 1.64 GHz with the matrix unit 68% busy: the chip's power sets the pace; weight
@@ -130,6 +130,34 @@ __device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stag
   }
 }
 
+// As store_block, in fp32: 64 rows of 256 bytes at a time fill a wave's 16 KB, chunk c of row r at c ^ (r & 15)
+// (32 lanes write one chunk of 32 rows: other banks), and go out as whole rows. (Straight from the registers,
+// 128 bytes of a row at a time, the planes of 4096 x 512 x 5 took 24 us more.)
+__device__ __forceinline__ void store_block_f32(const v16f (&t)[4][2], uint8_t* stage, float* out, int ld, int rows, int cols, int r0,
+                                                int c0, int lane) {
+  const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+          const v16f& x = t[2 * half + ii][j];
+          const int row = ii * 32 + lr, c = 8 * j + v / 2 + lh;
+          *reinterpret_cast<float4*>(stage + row * 256 + 16 * (c ^ (row & 15))) = float4{x[v], x[v + 1], x[v + 2], x[v + 3]};
+        }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int rr = 4 * q + (lane >> 4), c = lane & 15;
+      const float4 val = *reinterpret_cast<const float4*>(stage + rr * 256 + 16 * (c ^ (rr & 15)));
+      const int row = r0 + half * 64 + rr, col = c0 + 4 * c;
+      if (row < rows && col < cols) *reinterpret_cast<float4*>(out + (size_t)row * ld + col) = val;
+    }
+  }
+}
+
 // The other way: 64 rows of one 32-column tile of a bf16 matrix -> stage (rows of 80 bytes), zeros outside.
 __device__ __forceinline__ void load_rows(const uint16_t* in, int ld, uint8_t* stage, int rows, int cols, int r0, int c0, int lane) {
   uint4 v[4];
@@ -146,7 +174,6 @@ template <int AM, int BM, int EPI, int ACT = 0>
 __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g) {
   constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
   constexpr bool PERM = BM == CODES;   // contraction order of a step: 16 h + 8 s + e instead of 16 s + 8 h + e
-  constexpr bool SWAP = EPI != OUT_F32;
   constexpr int NA = 4, NB = BM == CODES ? 3 : 4, NDMA = NA + NB;   // copies per copying wave and step
   static_assert(!GATED || (AM == ROWS && BM == ROWS), "gated: both operands by rows");
   __shared__ Slot sl0, sl1, sl2, sl3;
@@ -316,7 +343,7 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(SWAP ? b[j] : a[i]), as_bf16x8(SWAP ? a[i] : b[j]), acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(b[j]), as_bf16x8(a[i]), acc[i][j], 0, 0, 0);
   };
   // half a step's order: the next half's operands are read between this half's first matrix instructions
   auto order = [](auto copies) {
@@ -378,19 +405,9 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   const int r0 = m0 + 128 * wm;
   if constexpr (EPI == OUT_BF16) {
     store_block<0, 2>(acc, stage, static_cast<uint16_t*>(g.out[prob]), g.ldo, g.rows, g.cols, r0, n0 + 64 * wn, lane);
-  } else if constexpr (EPI == OUT_F32) {   // lane: column lr, rows 8 (v / 4) + 4 lh + v % 4 of each tile
-    float* out = static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int row = r0 + 32 * i + 8 * (v >> 2) + 4 * lh + (v & 3);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = n0 + 64 * wn + 32 * j + lr;
-          if (row < g.rows && col < g.cols) out[(size_t)row * g.ldo + col] = acc[i][j][v];
-        }
-      }
+  } else if constexpr (EPI == OUT_F32) {
+    store_block_f32(acc, stage, static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo, g.ldo, g.rows, g.cols, r0,
+                    n0 + 64 * wn, lane);
   } else {
     const int c0 = n0 + 32 * wn;
     if constexpr (EPI == OUT_GATED_GRAD) {   // dH's rows: 2 x 64 of them, 5 KB each
