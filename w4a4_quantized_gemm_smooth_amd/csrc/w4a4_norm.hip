@@ -475,9 +475,10 @@ hipError_t backward(const void* dY, int lddy, const void* X, int ldx, const void
   return hipGetLastError();
 }
 
-// A thread holds two rows' pieces (the current and the next) and the sums of its columns. A block is one
-// row's waves where that is more than one: blocks of several rows waited for each other's barriers (bf16
-// 16384 x 4096, two blocks a compute unit: four rows a block 116 us, two 89, one 84).
+// A thread holds two rows' pieces (the current and the next) and the sums of its columns, so two pieces a row
+// leave two blocks a compute unit their registers (bf16 16384 x 2048: two waves a row with two pieces 49 us, one
+// with four 60, four with one 58). A block is one or two rows' waves where a row has several: blocks of more
+// rows waited for each other's barriers (16384 x 4096: four rows a block 116 us, two 89, one 84).
 template <class T, class P>
 hipError_t dispatch_backward(const void* dY, int lddy, const void* X, int ldx, const void* gamma, const float* mean,
                              const float* rstd, int M, int K, void* dX, int lddx, float* dgamma, float* dbeta, float* part,
@@ -487,7 +488,7 @@ hipError_t dispatch_backward(const void* dY, int lddy, const void* X, int ldx, c
   return backward<T, P, wpr, c, waves>(dY, lddy, X, ldx, gamma, mean, rstd, M, K, dX, lddx, dgamma, dbeta, part, st)
   if (K <= W) W4A4_NB(1, 1, 8);
   if (K <= 2 * W) W4A4_NB(1, 2, 8);
-  if (K <= 4 * W) W4A4_NB(1, 4, 8);
+  if (K <= 4 * W) W4A4_NB(2, 2, 4);
   if (K <= 8 * W) W4A4_NB(4, 2, 4);
   if (K <= 16 * W) W4A4_NB(8, 2, 8);
   if (K <= 32 * W) W4A4_NB(8, 4, 8);
