@@ -429,7 +429,7 @@ def test_checkpoint_of_every_bf16_value():
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (31, 8, 64), (33, 264, 40), (64, 256, 256), (97, 40, 520), (300, 520, 264), (2049, 16, 1000),
                                    (1500, 128, 136), (1000, 136, 8), (5000, 32, 72), (2100, 64, 520),
-                                   (700, 72, 200), (1000, 200, 72)])
+                                   (700, 72, 200), (1000, 200, 72), (300, 2600, 2000)])
 def test_checkpoint_weight_grad(M, N, K, out):
     x, dy = _rand(M, (M, K)), _rand(N, (M, N), 0.1)
     codes, scales = _pack(x)
@@ -505,7 +505,7 @@ def _gated_backward(x, wg, wu, dh, act):
 
 
 GATED = [(1, 8, 8), (1, 512, 200), (2, 72, 40), (16, 1032, 264), (17, 40, 136), (33, 200, 72), (48, 136, 520), (49, 64, 64), (255, 64, 128), (300, 520, 392), (64, 2048, 1000),
-         (513, 96, 24), (2000, 256, 256), (1100, 2056, 1032)]
+         (513, 96, 24), (2000, 256, 256), (1100, 2056, 1032), (1500, 1000, 2600)]
 
 
 @gpu

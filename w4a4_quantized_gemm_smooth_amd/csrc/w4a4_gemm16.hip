@@ -41,10 +41,9 @@ namespace {
 enum : int { ROWS = 0, COLS = 1, CODES = 2 };
 enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_GATED = 2, OUT_GATED_GRAD = 3 };
 
-constexpr int TM = 256, TN = 256;   // block rows and columns
+constexpr int TILE = 256, SMALL_TILE = 128;   // block rows and columns (gated: half as many columns)
 constexpr int KSTEP = 32;        // contraction per step
 constexpr int NSLOT = 4;         // ring slots
-constexpr int GM_THREADS = 512;
 constexpr int GM_MAX_LD = 1 << 21;   // 256 rows stay below 2^31 bytes
 constexpr int RSRC_W3 = 0x00020000;
 constexpr int OOB = (int)0x80000000;
@@ -67,9 +66,10 @@ struct GemmArgs {
 // lie in the eight different 32-byte parts of 256 bytes
 __device__ __forceinline__ int cols_sw(int k) { return 4 * (k & 3); }
 
+template <int W>   // rows and columns of a block
 struct __attribute__((aligned(16))) Slot {
-  uint8_t a[TM * KSTEP * 2];
-  uint8_t b[TN * KSTEP * 2];
+  uint8_t a[W * KSTEP * 2];
+  uint8_t b[W * KSTEP * 2];
 };
 
 // act(g) and act'(g), without branches. GELU: Phi(-|g|) = (t/2) exp(P(t) - g^2/2), t = 1/(1 + |g|/(2 sqrt 2)),
@@ -103,13 +103,13 @@ __device__ __forceinline__ void act_of(float g, float& a, float& slope) {
 // The wave's 32-column tiles J0 .. J0 + NT - 1 of transposed results (a lane: row lane % 32 of each 32-row
 // tile, columns 8 (v / 4) + 4 (lane / 32) + v % 4), fp32 -> bf16 through LDS, in whole 16-byte pieces of
 // rows. `stage`: 64 rows of NT * 64 + 16 bytes. cols is a multiple of 8, rows are 16-byte aligned.
-template <int J0, int NT>
-__device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stage, uint16_t* out, int ld, int rows, int cols,
+template <int J0, int NT, int MT>
+__device__ __forceinline__ void store_block(const v16f (&t)[MT][2], uint8_t* stage, uint16_t* out, int ld, int rows, int cols,
                                             int r0, int c0, int lane) {
   constexpr int ES = NT * 64 + 16, CPR = NT * 4;
   const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < MT / 2; ++half) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -133,11 +133,12 @@ __device__ __forceinline__ void store_block(const v16f (&t)[4][2], uint8_t* stag
 // As store_block, in fp32: 64 rows of 256 bytes at a time fill a wave's 16 KB, chunk c of row r at c ^ (r & 15)
 // (32 lanes write one chunk of 32 rows: other banks), and go out as whole rows. (Straight from the registers,
 // 128 bytes of a row at a time, the planes of 4096 x 512 x 5 took 24 us more.)
-__device__ __forceinline__ void store_block_f32(const v16f (&t)[4][2], uint8_t* stage, float* out, int ld, int rows, int cols, int r0,
+template <int MT>
+__device__ __forceinline__ void store_block_f32(const v16f (&t)[MT][2], uint8_t* stage, float* out, int ld, int rows, int cols, int r0,
                                                 int c0, int lane) {
   const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < MT / 2; ++half) {
 #pragma unroll
     for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -170,63 +171,79 @@ __device__ __forceinline__ void load_rows(const uint16_t* in, int ld, uint8_t* s
   for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + (16 * q + (lane >> 2)) * 80 + 16 * (lane & 3)) = v[q];
 }
 
-template <int AM, int BM, int EPI, int ACT = 0>
-__global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g) {
+// One LDS DMA instruction: 16 or 4 bytes a lane to consecutive places from dst on. (Functions of their own: with
+// arguments that depend on a kernel's template parameters in the builtin's own list, the host pass loses
+// the kernel's launch stub.)
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t* dst, int offset, int scalar) {
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 16, offset, scalar, 0, 0);
+}
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, int offset, int scalar) {
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)dst, 4, offset, scalar, 0, 0);
+}
+
+// SMALL: blocks of 128 x 128, four waves of 64 x 64, two blocks to a compute unit; the same otherwise.
+template <int AM, int BM, int EPI, int ACT, bool SMALL>
+__global__ __launch_bounds__(SMALL ? 256 : 512, SMALL ? 2 : 1) void gemm16_kernel(const GemmArgs g) {
   constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
   constexpr bool PERM = BM == CODES;   // contraction order of a step: 16 h + 8 s + e instead of 16 s + 8 h + e
-  constexpr int NA = 4, NB = BM == CODES ? 3 : 4, NDMA = NA + NB;   // copies per copying wave and step
+  constexpr int W = SMALL ? SMALL_TILE : TILE, MT = SMALL ? 2 : 4, WN = W / 64;   // 32-row tiles of a wave, waves along N
+  constexpr int NA = W / 64, NB = BM == CODES ? NA / 2 + 1 : NA, NDMA = NA + NB;   // copies per copying wave and step
+  constexpr int RB = W * 2, CPR = W / 8;                                           // COLS: bytes and chunks of an LDS row
   static_assert(!GATED || (AM == ROWS && BM == ROWS), "gated: both operands by rows");
-  __shared__ Slot sl0, sl1, sl2, sl3;
-  Slot* const ring[NSLOT] = {&sl0, &sl1, &sl2, &sl3};
-  typedef __attribute__((address_space(3))) void* lds_ptr;
+  __shared__ Slot<W> sl0, sl1, sl2, sl3;
+  Slot<W>* const ring[NSLOT] = {&sl0, &sl1, &sl2, &sl3};
   typedef __attribute__((address_space(3))) v4s* lds_v4s;
 
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, lh = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
-  const int tiles_n = (g.cols + (GATED ? TN / 2 : TN) - 1) / (GATED ? TN / 2 : TN), tiles_mp = (g.rows + TM - 1) / TM;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN, cw = wave & 3;
+  constexpr int WC = GATED ? W / 2 : W;
+  const int tiles_n = (g.cols + WC - 1) / WC, tiles_mp = (g.rows + W - 1) / W;
   int tm, tn;
   tile_of(blockIdx.x, gridDim.x, tiles_mp * g.probs, tiles_n, tm, tn);
-  const int prob = tm / tiles_mp, m0 = (tm % tiles_mp) * TM, n0 = tn * (GATED ? TN / 2 : TN);
+  const int prob = tm / tiles_mp, m0 = (tm % tiles_mp) * W, n0 = tn * WC;
   const int all = g.steps * g.segs, s_lo = (int)((long long)all * blockIdx.y / g.splits),
             s_hi = (int)((long long)all * (blockIdx.y + 1) / g.splits), S = s_hi - s_lo;
 
-  // ---- copies: instruction q of copying wave wn fills the KB 4 wn + q of an operand; the lane's source
+  // ---- copies: instruction q of copying wave cw fills the KB t = NA cw + q of an operand; the lane's source
   // offset (with OOB), and its contraction index in the step
-  int va[NA], vb[4];
+  int va[NA], vb[NA];
   const int kc = 8 * ((lane & 3) ^ ((lane >> 4) & 3));   // ROWS: 16 rows an instruction, this lane's chunk
   const int ra4 = lane >> 2;
-  auto krow = [&](int t) { return 2 * t + (lane >> 5); };   // COLS: two rows an instruction
-  auto kcol = [&](int t) { return 8 * ((lane & 31) ^ cols_sw(krow(t))); };
+  auto krow = [&](int t) { return 64 / CPR * t + lane / CPR; };   // COLS: two or four rows an instruction
+  auto kcol = [&](int t) { return 8 * ((lane % CPR) ^ cols_sw(krow(t))); };
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
-    const int t = 4 * wn + q;
+    const int t = NA * cw + q;
     if constexpr (AM == ROWS)
       va[q] = ((16 * t + ra4) * g.lda + kc) * 2 | (m0 + 16 * t + ra4 < g.rows ? 0 : OOB);
     else
       va[q] = (krow(t) * g.lda + kcol(t)) * 2 | (m0 + kcol(t) < g.rows ? 0 : OOB);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int t = 4 * wn + q;
-    if constexpr (GATED) {   // a wave's 64 rows: 32 of the one weight, 32 of the other
-      const int row = 32 * wn + 16 * (q & 1) + ra4;
+  for (int q = 0; q < NA; ++q) {
+    const int t = NA * cw + q;
+    if constexpr (GATED) {   // a wave's 64 rows: 32 of the one weight (t / 2 even), 32 of the other
+      const int row = 32 * (t >> 2) + 16 * (t & 1) + ra4;
       vb[q] = (row * g.ldb + kc) * 2 | (n0 + row < g.cols ? 0 : OOB);
     } else if constexpr (BM == ROWS) {
       vb[q] = ((16 * t + ra4) * g.ldb + kc) * 2 | (n0 + 16 * t + ra4 < g.cols ? 0 : OOB);
     } else if constexpr (BM == COLS) {
       vb[q] = (krow(t) * g.ldb + kcol(t)) * 2 | (n0 + kcol(t) < g.cols ? 0 : OOB);
-    } else {
-      const int row = 64 * wn + 32 * (q & 1) + (lane >> 1);
+    } else {   // NA / 2 of them
+      const int row = 32 * (NA / 2 * cw + q % (NA / 2)) + (lane >> 1);
       vb[q] = (row * 32 + 16 * ((lane & 1) ^ ((row >> 3) & 1))) | (n0 + row < g.cols ? 0 : OOB);
     }
   }
-  const int vs = (64 * wn + 4 * (lane & 15)) | (n0 + 64 * wn + 4 * (lane & 15) < g.cols ? 0 : OOB);   // CODES: 64 scales
+  // CODES: this wave's W / 4 scales
+  const int vs = (W / 4 * cw + 4 * (lane & 15)) | (n0 + W / 4 * cw + 4 * (lane & 15) < g.cols ? 0 : OOB);
   // every offset outside an operand carries OOB, so the descriptors need no range of their own
   auto rsrc = [](const void* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7FFFFFFF, RSRC_W3); };
   // ROWS: a step moves the scalar offset (a row is below 2^22 bytes); COLS: the 64-bit base.
   auto rows_at = [&](const void* p, int ld, int first) { return rsrc(static_cast<const uint16_t*>(p) + (size_t)first * ld); };
   auto cols_at = [&](const void* p, int ld, int first, int k0) { return rsrc(static_cast<const uint16_t*>(p) + (size_t)k0 * ld + first); };
-  auto dma_a = [&](int i, Slot* sl) {   // step i of this block's; past the end: zeros
+  auto dma_a = [&](int i, Slot<W>* sl) {   // step i of this block's; past the end: zeros
     const int s = s_lo + min(i, S - 1), past = i < S ? 0 : OOB, seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
     const int kin = past | (k0 + kc < g.K ? 0 : OOB);
     auto in = [&](int t) { return past | (k0 + krow(t) < g.K ? 0 : OOB); };
@@ -234,48 +251,49 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       const __amdgpu_buffer_rsrc_t r = rows_at(g.A[prob + seg], g.lda, m0);
 #pragma unroll
       for (int q = 0; q < NA; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * wn + q)), 16, va[q] | kin, k0 * 2, 0, 0);
+        copy16(r, sl->a + 1024 * (NA * cw + q), va[q] | kin, k0 * 2);
     } else {
       const __amdgpu_buffer_rsrc_t r = cols_at(g.A[prob + seg], g.lda, m0, k0);
 #pragma unroll
-      for (int q = 0; q < NA; ++q) {   // (no call in the builtin's arguments: the host pass would lose the kernel's stub)
-        const int v = va[q] | in(4 * wn + q);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->a + 1024 * (4 * wn + q)), 16, v, 0, 0, 0);
+      for (int q = 0; q < NA; ++q) {
+        const int v = va[q] | in(NA * cw + q);
+        copy16(r, sl->a + 1024 * (NA * cw + q), v, 0);
       }
     }
   };
-  auto dma_b = [&](int i, Slot* sl) {
+  auto dma_b = [&](int i, Slot<W>* sl) {
     const int s = s_lo + min(i, S - 1), past = i < S ? 0 : OOB, seg = s >= g.steps ? 1 : 0, k0 = (s - seg * g.steps) * KSTEP;
     const int kin = past | (k0 + kc < g.K ? 0 : OOB);
     auto in = [&](int t) { return past | (k0 + krow(t) < g.K ? 0 : OOB); };
     if constexpr (GATED) {
-      const __amdgpu_buffer_rsrc_t r0 = rows_at(g.B[0], g.ldb, n0), r1 = rows_at(g.B[1], g.ldb, n0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < 2 ? r0 : r1, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, vb[q] | kin, k0 * 2, 0, 0);
+      for (int q = 0; q < NA; ++q) {
+        const __amdgpu_buffer_rsrc_t r = rows_at(g.B[((NA * cw + q) >> 1) & 1], g.ldb, n0);
+        copy16(r, sl->b + 1024 * (NA * cw + q), vb[q] | kin, k0 * 2);
+      }
     } else if constexpr (BM == ROWS) {
       const __amdgpu_buffer_rsrc_t r = rows_at(g.B[seg], g.ldb, n0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, vb[q] | kin, k0 * 2, 0, 0);
+      for (int q = 0; q < NA; ++q)
+        copy16(r, sl->b + 1024 * (NA * cw + q), vb[q] | kin, k0 * 2);
     } else if constexpr (BM == COLS) {
       const __amdgpu_buffer_rsrc_t r = cols_at(g.B[seg], g.ldb, n0, k0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int v = vb[q] | in(4 * wn + q);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (4 * wn + q)), 16, v, 0, 0, 0);
+      for (int q = 0; q < NA; ++q) {
+        const int v = vb[q] | in(NA * cw + q);
+        copy16(r, sl->b + 1024 * (NA * cw + q), v, 0);
       }
     } else {
       const size_t c = (size_t)s * g.cols + n0;
       const __amdgpu_buffer_rsrc_t r = rsrc(static_cast<const uint8_t*>(g.B[0]) + c * 32), rs = rsrc(g.scales + c);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sl->b + 1024 * (2 * wn + q)), 16, vb[q] | past, 0, 0, 0);
-      if (lane < 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(sl->b + 8192 + 64 * wn), 4, vs | past, 0, 0, 0);
+      for (int q = 0; q < NA / 2; ++q)
+        copy16(r, sl->b + 1024 * (NA / 2 * cw + q), vb[q] | past, 0);
+      if (lane < W / 16) copy4(rs, sl->b + W * 32 + W / 4 * cw, vs | past, 0);
     }
   };
 
-  auto dma = [&](int i, Slot* sl) {
+  auto dma = [&](int i, Slot<W>* sl) {
     dma_a(i, sl);
     dma_b(i, sl);
   };
@@ -286,13 +304,13 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   for (int i = 0; i < 4; ++i) {
     const int i16 = lane & 15, mh = (lane >> 4) & 1, kk = (PERM ? 16 : 8) * lh + (i16 >> 2), sw = cols_sw(kk);
     if (AM == ROWS)
-      ra[i] = (128 * wm + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
+      ra[i] = (32 * MT * wm + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
     else
-      ra[i] = kk * 512 + 16 * ((16 * wm + 4 * i + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
+      ra[i] = kk * RB + 16 * ((4 * MT * wm + 4 * (i % MT) + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
     if (BM == ROWS)
       rb[i] = (64 * wn + lr) * 64 + 16 * ((2 * (i & 1) + lh) ^ ((lr >> 2) & 3));
     else if (BM == COLS)
-      rb[i] = kk * 512 + 16 * ((8 * wn + 4 * (i & 1) + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
+      rb[i] = kk * RB + 16 * ((8 * wn + 4 * (i & 1) + 2 * mh + ((i16 & 3) >> 1)) ^ sw) + 8 * (i16 & 1);
     else
       rb[i] = sw_off32(64 * wn + lr, lh) + 1024 * (i & 1);
   }
@@ -300,25 +318,25 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
   auto two = [](v2i x, v2i y) { return v4i{x[0], x[1], y[0], y[1]}; };
   v4i code[2];      // CODES: a lane's 16 codes of a step, both sub-steps', read with the first
   float scale[2];   // 2^e from its byte: 0 is the subnormal 2^-127; 255 gives Inf, and NaN with its codes of 0
-  auto rd = [&](Slot* sl, int s, v4i (&A)[4], v4i (&B)[2]) {
+  auto rd = [&](Slot<W>* sl, int s, v4i (&A)[MT], v4i (&B)[2]) {
     constexpr int SUB = PERM ? 8 : 16;   // contraction rows from sub-step 0 to 1 in a COLS slot
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < MT; ++i) {
       if constexpr (AM == ROWS)
         A[i] = *reinterpret_cast<const v4i*>(sl->a + ra[s] + 2048 * i);
       else
-        A[i] = two(tr(sl->a + ra[i] + SUB * 512 * s), tr(sl->a + ra[i] + SUB * 512 * s + 4 * 512));
+        A[i] = two(tr(sl->a + ra[i] + SUB * RB * s), tr(sl->a + ra[i] + SUB * RB * s + 4 * RB));
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (BM == ROWS) {
         B[j] = *reinterpret_cast<const v4i*>(sl->b + rb[s] + 2048 * j);
       } else if constexpr (BM == COLS) {
-        B[j] = two(tr(sl->b + rb[j] + SUB * 512 * s), tr(sl->b + rb[j] + SUB * 512 * s + 4 * 512));
+        B[j] = two(tr(sl->b + rb[j] + SUB * RB * s), tr(sl->b + rb[j] + SUB * RB * s + 4 * RB));
       } else {
         if (s == 0) {
           code[j] = *reinterpret_cast<const v4i*>(sl->b + rb[j]);
-          const uint32_t e = sl->b[8192 + 64 * wn + 32 * j + lr];
+          const uint32_t e = sl->b[W * 32 + 64 * wn + 32 * j + lr];
           scale[j] = __uint_as_float(max(e << 23, 0x00400000u));
         }
 #pragma unroll
@@ -331,36 +349,36 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
     }
   };
 
-  v16f acc[4][2];
+  v16f acc[MT][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-  auto mfmas = [&](const v4i (&a)[4], const v4i (&b)[2]) {
+  auto mfmas = [&](const v4i (&a)[MT], const v4i (&b)[2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(b[j]), as_bf16x8(a[i]), acc[i][j], 0, 0, 0);
   };
   // half a step's order: the next half's operands are read between this half's first matrix instructions
   auto order = [](auto copies) {
-    constexpr int NRD = (AM == COLS ? 8 : 4) + (BM == COLS ? 4 : BM == ROWS ? 2 : 4), PER = (NRD + 5) / 6;
+    constexpr int Q = 2 * MT - 2, NRD = (AM == COLS ? 2 * MT : MT) + (BM == COLS ? 4 : BM == ROWS ? 2 : 4), PER = (NRD + Q - 1) / Q;
 #pragma unroll
-    for (int q = 0; q < 6; ++q) {
+    for (int q = 0; q < Q; ++q) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // one MFMA
       __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);   // LDS reads
     }
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);   // copies
+    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, copies.value / 2, 0);   // copies
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, copies.value - 2, 0);
+    if (copies.value) __builtin_amdgcn_sched_group_barrier(0x020, copies.value - copies.value / 2, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  v4i A[2][4], B[2][2];
-  const bool copies = wave < 4;
+  v4i A[2][MT], B[2][2];
+  const bool copies = SMALL || wave < 4;
   if (copies) {
 #pragma unroll
     for (int i = 0; i < NSLOT - 1; ++i) dma(i, ring[i]);
@@ -389,20 +407,24 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
       }
     }
   };
-  if (copies)
+  if constexpr (SMALL) {
     main_loop(std::true_type{});
-  else
-    main_loop(std::false_type{});
+  } else {
+    if (copies)
+      main_loop(std::true_type{});
+    else
+      main_loop(std::false_type{});
+  }
   wait_vmcnt<0>();   // no LDS DMA may outlive the block
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 
   // ---- epilogue
-  uint8_t* stage = nullptr;
+  uint8_t* stage = nullptr;   // 16 KB to a wave: a slot, or half of one
 #pragma unroll
-  for (int w = 0; w < 8; ++w)
-    if (wave == w) stage = (w & 1) ? ring[w >> 1]->b : ring[w >> 1]->a;   // 16 KB to a wave
-  const int r0 = m0 + 128 * wm;
+  for (int w = 0; w < 2 * WN; ++w)
+    if (wave == w) stage = SMALL ? ring[w % NSLOT]->a : (w & 1) ? ring[w >> 1]->b : ring[w >> 1]->a;
+  const int r0 = m0 + 32 * MT * wm;
   if constexpr (EPI == OUT_BF16) {
     store_block<0, 2>(acc, stage, static_cast<uint16_t*>(g.out[prob]), g.ldo, g.rows, g.cols, r0, n0 + 64 * wn, lane);
   } else if constexpr (EPI == OUT_F32) {
@@ -410,12 +432,12 @@ __global__ __launch_bounds__(GM_THREADS, 1) void gemm16_kernel(const GemmArgs g)
                     n0 + 64 * wn, lane);
   } else {
     const int c0 = n0 + 32 * wn;
-    if constexpr (EPI == OUT_GATED_GRAD) {   // dH's rows: 2 x 64 of them, 5 KB each
-      load_rows(g.dH, g.lddh, stage, g.rows, g.cols, r0, c0, lane);
-      load_rows(g.dH, g.lddh, stage + 64 * 80, g.rows, g.cols, r0 + 64, c0, lane);
+    if constexpr (EPI == OUT_GATED_GRAD) {   // dH's rows: 64 of them at a time, 5 KB
+#pragma unroll
+      for (int h = 0; h < MT / 2; ++h) load_rows(g.dH, g.lddh, stage + h * 64 * 80, g.rows, g.cols, r0 + 64 * h, c0, lane);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int v0 = 0; v0 < 16; v0 += 4) {
         uint2 d = {0u, 0u};
@@ -666,11 +688,15 @@ __global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16
 inline int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
 template <int AM, int BM, int EPI, int ACT = 0>
-hipError_t launch(const GemmArgs& g, hipStream_t st) {
+hipError_t launch(const GemmArgs& g, bool small, hipStream_t st) {
   constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
-  const long long blocks = (long long)tiles_of(g.rows, TM) * g.probs * tiles_of(g.cols, GATED ? TN / 2 : TN);
+  const int w = small ? SMALL_TILE : TILE;
+  const long long blocks = (long long)tiles_of(g.rows, w) * g.probs * tiles_of(g.cols, GATED ? w / 2 : w);
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI, ACT>), dim3((unsigned)blocks, g.splits), dim3(GM_THREADS), 0, st, g);
+  if (small)
+    hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI, ACT, true>), dim3((unsigned)blocks, g.splits), dim3(256), 0, st, g);
+  else
+    hipLaunchKernelGGL((gemm16_kernel<AM, BM, EPI, ACT, false>), dim3((unsigned)blocks, g.splits), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -681,18 +707,31 @@ hipError_t join(const float* part, int splits, long long n, T* out, hipStream_t 
   return hipGetLastError();
 }
 
-// Parts of the contraction, so that a few blocks fill the chip: the number that a simple cost favours.
-// Measured: a step of a round of 256 blocks 0.6 us (0.9 where the chip's power limits it: all blocks at
-// length); a value of a plane, written and read by the join, 8 bytes at 6 TB/s, and 6 us for the join's
-// launch. Parts are at least 4 steps long.
-int splits_of(long long blocks, int steps, double values) {
-  int best = 1;
+// How a product is cut: blocks of 256 or 128, and parts of its contraction (to planes of `values` fp32 each,
+// added by the join; 0: it cannot be split), whichever a simple cost favours. Measured: a round of large blocks
+// (256) 0.6 us a step (0.9 at the chip's power limit: all blocks at length) and 8 us besides, of small ones
+// (512, two to a compute unit) 0.45 us (0.35 up to 256; with codes, which each wave converts for half as many
+// rows, 0.75 and 0.5) and 5 us; a plane's value, written and read, 8 bytes at 6 TB/s; 6 us for the join's launch.
+// Parts are at least 4 steps long. Both sides (calls, us, large / small): gated forward 300 x 520 x 392 15.8 /
+// 9.7, 128 x 4096 x 12288 91 / 63, 2048 x 1024 x 4096 35 / 47; backward 1000 x 1024 x 2816 81 / 73, 2041 x 2056 x
+// 5624 334 / 398; weight gradient 200 x 8192 from 8192 tokens 53 / 67.
+struct Plan {
+  bool small;
+  int splits;
+};
+Plan plan_of(int rows, int probs, int cols, bool gated, bool codes, int steps, double values) {
+  Plan best{false, 1};
   double least = 0.;
-  for (int s = 1; s == 1 || (s <= steps / 4 && s <= 64 && blocks * s <= 512); ++s) {
-    const double t = 0.6 * (double)((blocks * s + 255) / 256) * ((steps + s - 1) / s) + (s > 1 ? 6. + s * values * 8. / 6e6 : 0.);
-    if (s == 1 || t < least) {
-      least = t;
-      best = s;
+  for (int small = 0; small < 2; ++small) {
+    const int w = small ? SMALL_TILE : TILE, round = small ? 512 : 256;
+    const long long blocks = (long long)tiles_of(rows, w) * probs * tiles_of(cols, gated ? w / 2 : w);
+    for (int s = 1; s == 1 || (values > 0. && s <= steps / 4 && s <= 64 && blocks * s <= 2 * round); ++s) {
+      const double rounds = (double)((blocks * s + round - 1) / round), step = !small ? 0.6 : blocks * s <= 256 ? (codes ? 0.5 : 0.35) : codes ? 0.75 : 0.45;
+      const double t = rounds * (step * ((steps + s - 1) / s) + (small ? 5. : 8.)) + (s > 1 ? 6. + s * values * 8. / 6e6 : 0.);
+      if ((small == 0 && s == 1) || t < least) {
+        least = t;
+        best = Plan{small == 1, s};
+      }
     }
   }
   return best;
@@ -711,7 +750,7 @@ size_t matrix_bytes(int rows, int cols) { return ((size_t)rows * pad32(cols) * 2
 // Only where the steps' extra time (measured: 0.35 us a step of a round of 256 blocks) clearly exceeds the copy's.
 size_t gated_pad_bytes(int M, int K, int F) {
   if (K % 32 == 0 || M <= GT_MAX_M) return 0;
-  const double rounds = (double)(((long long)tiles_of(M, TM) * tiles_of(F, TN / 2) + 255) / 256);
+  const double rounds = (double)(((long long)tiles_of(M, TILE) * tiles_of(F, TILE / 2) + 255) / 256);
   const double extra = 0.35 * rounds * tiles_of(K, KSTEP), copy = 6. + ((double)M + 2. * F) * K * 4. / 5e6;
   return extra < 1.3 * copy ? 0 : matrix_bytes(M, K) + 2 * matrix_bytes(F, K);
 }
@@ -741,12 +780,9 @@ hipError_t gated_operands(const uint16_t* X, int M, int K, int ldx, const uint16
   hipLaunchKernelGGL(pad_rows_kernel, dim3(1024, 3), dim3(256), 0, st, a);
   return hipGetLastError();
 }
-int gated_dx_splits(int M, int K, int F) {
-  return splits_of((long long)tiles_of(M, TM) * tiles_of(K, TN), 2 * tiles_of(F, KSTEP), (double)M * K);
-}
-int gated_dw_splits(int M, int K, int F) {
-  return splits_of(2LL * tiles_of(F, TM) * tiles_of(K, TN), tiles_of(M, KSTEP), 2. * F * K);
-}
+Plan gated_plan(int M, int K, int F) { return plan_of(M, 1, F, true, false, tiles_of(K, KSTEP), 0.); }
+Plan gated_dx_plan(int M, int K, int F) { return plan_of(M, 1, K, false, false, 2 * tiles_of(F, KSTEP), (double)M * K); }
+Plan gated_dw_plan(int M, int K, int F) { return plan_of(F, 2, K, false, false, tiles_of(M, KSTEP), 2. * F * K); }
 
 }  // namespace
 
@@ -782,14 +818,16 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
     g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = H;
     g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
     g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
-    e = act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_SILU>(g, st) : launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_GELU>(g, st);
+    const bool small = gated_plan(M, K, F).small;
+    e = act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_SILU>(g, small, st)
+                             : launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_GELU>(g, small, st);
   }
   return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
 }
 
 size_t w4a4_gated_backward_bytes(int M, int K, int F) {
   if (!gated_shape_ok(M, K, F)) return 0;
-  const int sx = gated_dx_splits(M, K, F), sw = gated_dw_splits(M, K, F);
+  const int sx = gated_dx_plan(M, K, F).splits, sw = gated_dw_plan(M, K, F).splits;
   const size_t px = sx > 1 ? (size_t)sx * M * K * 4 : 0, pw = sw > 1 ? (size_t)sw * 2 * F * K * 4 : 0;
   return gated_pad_bytes(M, K, F) + 2 * gated_hidden_bytes(M, F) + (px > pw ? px : pw);
 }
@@ -816,38 +854,42 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
   g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
   g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldg, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
   g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
-  if ((act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_SILU>(g, st)
-                            : launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_GELU>(g, st)) != hipSuccess)
+  const bool small = gated_plan(M, K, F).small;
+  if ((act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_SILU>(g, small, st)
+                            : launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_GELU>(g, small, st)) != hipSuccess)
     return W4A4_ERR_HIP;
 
   GemmArgs x{};   // dX = [dG dU] [Wg; Wu]
   x.A[0] = dG, x.A[1] = dU, x.B[0] = o.wg, x.B[1] = o.wu;
   x.lda = ldg, x.ldb = o.ldw, x.ldo = K, x.rows = M, x.cols = K, x.K = F;
-  x.segs = 2, x.probs = 1, x.steps = tiles_of(F, KSTEP), x.splits = gated_dx_splits(M, K, F);
+  const Plan px = gated_dx_plan(M, K, F);
+  x.segs = 2, x.probs = 1, x.steps = tiles_of(F, KSTEP), x.splits = px.splits;
   x.out[0] = x.splits > 1 ? static_cast<void*>(planes) : dX;
-  if ((x.splits > 1 ? launch<ROWS, COLS, OUT_F32>(x, st) : launch<ROWS, COLS, OUT_BF16>(x, st)) != hipSuccess) return W4A4_ERR_HIP;
+  if ((x.splits > 1 ? launch<ROWS, COLS, OUT_F32>(x, px.small, st) : launch<ROWS, COLS, OUT_BF16>(x, px.small, st)) != hipSuccess)
+    return W4A4_ERR_HIP;
   if (x.splits > 1 && join(planes, x.splits, (long long)M * K, dX, st) != hipSuccess) return W4A4_ERR_HIP;
 
   GemmArgs w{};   // dWg = dG^T X, dWu = dU^T X
   w.A[0] = dG, w.A[1] = dU, w.B[0] = o.x, w.out[0] = dWg, w.out[1] = dWu;
   w.lda = ldg, w.ldb = o.ldx, w.ldo = K, w.rows = F, w.cols = K, w.K = M;
-  w.segs = 1, w.probs = 2, w.splits = gated_dw_splits(M, K, F), w.steps = tiles_of(M, KSTEP);
-  if (w.splits == 1) return launch<COLS, COLS, OUT_BF16>(w, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
+  const Plan pw = gated_dw_plan(M, K, F);
+  w.segs = 1, w.probs = 2, w.splits = pw.splits, w.steps = tiles_of(M, KSTEP);
+  if (w.splits == 1) return launch<COLS, COLS, OUT_BF16>(w, pw.small, st) == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
   const long long n = (long long)F * K;
   w.out[0] = planes, w.out[1] = planes + w.splits * n;
-  const bool ok = launch<COLS, COLS, OUT_F32>(w, st) == hipSuccess && join(planes, w.splits, n, dWg, st, dWu) == hipSuccess;
+  const bool ok = launch<COLS, COLS, OUT_F32>(w, pw.small, st) == hipSuccess && join(planes, w.splits, n, dWg, st, dWu) == hipSuccess;
   return ok ? W4A4_OK : W4A4_ERR_HIP;
 }
 
 // Rows of dW up to which factor_grad_kernel is used, against the product kernel (calls, us): 32 x 8192 from 8192
 // tokens 20 / 39, 72 x 4096 from 4608 18 / 25, 128 x 8192 from 8192 40 / 49.
 constexpr int FACTOR_MAX_N = 128;
-static int weight_grad_splits(int M, int N, int K) {
+static Plan weight_grad_plan(int M, int N, int K) {
   if (N <= FACTOR_MAX_N) {   // a block to each compute unit, a token block at least to every wave
     const int s = (256 + tiles_of(K, 64) - 1) / tiles_of(K, 64), most = tiles_of(tiles_of(M, W4A4_CHECKPOINT_BLOCK), FG_WAVES);
-    return s < most ? s : most;
+    return Plan{false, s < most ? s : most};
   }
-  return splits_of((long long)tiles_of(N, TM) * tiles_of(K, TN), tiles_of(M, KSTEP), (double)N * K);
+  return plan_of(N, 1, K, false, true, tiles_of(M, KSTEP), (double)N * K);
 }
 static bool weight_grad_shape_ok(int M, int N, int K) {
   return checkpoint_shape_ok(M, K) && N >= 8 && N % 8 == 0 && N <= GM_MAX_LD && K <= GM_MAX_LD;
@@ -855,7 +897,7 @@ static bool weight_grad_shape_ok(int M, int N, int K) {
 
 size_t w4a4_checkpoint_weight_grad_bytes(int M, int N, int K) {
   if (!weight_grad_shape_ok(M, N, K)) return 0;
-  return (size_t)weight_grad_splits(M, N, K) * N * K * 4;
+  return (size_t)weight_grad_plan(M, N, K).splits * N * K * 4;
 }
 
 w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const int8_t* codes, const uint8_t* scales, int M,
@@ -869,7 +911,8 @@ w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const in
   GemmArgs g{};
   g.A[0] = dY, g.B[0] = codes, g.scales = scales;
   g.lda = lddy, g.ldo = K, g.rows = N, g.cols = K, g.K = M;
-  g.segs = g.probs = 1, g.steps = tiles_of(M, KSTEP), g.splits = weight_grad_splits(M, N, K);
+  const Plan plan = weight_grad_plan(M, N, K);
+  g.segs = g.probs = 1, g.steps = tiles_of(M, KSTEP), g.splits = plan.splits;
   hipError_t e;
   if (N <= FACTOR_MAX_N) {
     float* planes = static_cast<float*>(ws);
@@ -889,11 +932,11 @@ w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const in
                                       : join(planes, g.splits, (long long)N * K, static_cast<uint16_t*>(dW), st);
   } else if (g.splits == 1) {
     g.out[0] = dW;
-    e = out_dtype == W4A4_DTYPE_F32 ? launch<COLS, CODES, OUT_F32>(g, st) : launch<COLS, CODES, OUT_BF16>(g, st);
+    e = out_dtype == W4A4_DTYPE_F32 ? launch<COLS, CODES, OUT_F32>(g, plan.small, st) : launch<COLS, CODES, OUT_BF16>(g, plan.small, st);
   } else {
     float* planes = static_cast<float*>(ws);
     g.out[0] = planes;
-    e = launch<COLS, CODES, OUT_F32>(g, st);
+    e = launch<COLS, CODES, OUT_F32>(g, plan.small, st);
     if (e == hipSuccess)
       e = out_dtype == W4A4_DTYPE_F32 ? join(planes, g.splits, (long long)N * K, static_cast<float*>(dW), st)
                                       : join(planes, g.splits, (long long)N * K, static_cast<uint16_t*>(dW), st);
