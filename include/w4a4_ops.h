@@ -107,7 +107,7 @@ w4a4_status_t w4a4_checkpoint_weight_grad(const uint16_t* dY, int lddy, const in
  *   dG = bf16(dH U act'(G)), dU = bf16(dH act(G)), dX = dG·Wg + dU·Wu, dWg = dG^T·X, dWu = dU^T·X.
  *   X [M][ldx], Wg and Wu [F][ldw], H and dH [M][ld >= F]; K and F multiples of 8, row strides multiples
  *   of 8 up to 2^21; dX [M][K], dWg and dWu [F][K] contiguous. G and U are computed again in the backward
- *   pass (they are not kept). M >= 1; up to 48 rows the forward pass has a kernel for few tokens.
+ *   pass (they are not kept). M >= 1; up to 32 rows the forward pass has a kernel for few tokens.
  *   ws   w4a4_gated_forward_bytes / w4a4_gated_backward_bytes (M, K, F) bytes (may be NULL where 0).
  * W4A4_ERR_UNSUPPORTED for an unknown act.
  */

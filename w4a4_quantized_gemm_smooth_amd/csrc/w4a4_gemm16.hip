@@ -8,11 +8,12 @@
 // its own.
 //
 // The product kernel. Blocks of 256 x 256 outputs, eight waves of 128 x 64 (4 x 2 tiles of 32x32, 128
-// accumulators to a lane). A step is 32 of the contraction: 16 KB an operand in one of four ring slots in
-// LDS, copied global -> LDS by the LDS DMA path of waves 0..3 (one a SIMD, so that an issue that stalls
-// holds up one of the SIMD's two waves) three steps ahead; the operands of half a step (16 of the
-// contraction) are read between the matrix instructions of the half before. Operands are copied as they
-// lie in memory, whichever of their axes is contiguous:
+// accumulators to a lane); where few of those would run, of 128 x 128 and four waves (plan_of). A step of
+// the large block is 32 of the contraction: 16 KB an operand in one of four ring slots in LDS, copied
+// global -> LDS by the LDS DMA path of waves 0..3 (one a SIMD, so that an issue that stalls holds up one
+// of the SIMD's two waves) three steps ahead; the operands of half a step (16 of the contraction) are
+// read between the matrix instructions of the half before. Operands are copied as they lie in memory,
+// whichever of their axes is contiguous:
 //   ROWS   contraction contiguous: LDS row = output row, 64 bytes of contraction; a lane's operand (8 of
 //          the contraction) is one 16-byte read. Chunk c of row r is kept at c ^ ((r >> 2) & 3).
 //   COLS   output axis contiguous: LDS row = one of the contraction, 512 bytes of the output axis; a
@@ -24,11 +25,11 @@
 // sizes cost nothing in the loop. Results are computed transposed (B as the first operand), which leaves a
 // lane four neighbouring columns of a row.
 //
-// Measured: gated forward 4608 x 4096 x 12288 787 us = 1180 TFLOP/s (the library's product of the same size
+// Measured: gated forward 4608 x 4096 x 12288 774 us = 1200 TFLOP/s (the library's product of the same size
 // 1084, its 8192^3 1290), at 1.64 GHz with the matrix unit 68% busy: the chip's power sets the pace; weight
-// gradient 4096 x 12288 from 4608 tokens' codes 455 us = 1020 TFLOP/s (the library's products of transposed
+// gradient 4096 x 12288 from 4608 tokens' codes 452 us = 1030 TFLOP/s (the library's products of transposed
 // operands 1006 to 1089). Small grids are bound by rounds of blocks: gradients 2041 x 2056 x 5624 in 20
-// (rows laid out anew) + 115 + 129 + 10 + 96 us.
+// (rows laid out anew) + 118 + 92 + 10 + 88 us.
 #include <type_traits>
 
 #include "w4a4_device_common.h"
@@ -509,7 +510,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const PadArgs a) {
 // token block's codes as the matrix operand needs them (16 of a channel's 32 tokens), and dY's 32 tokens go
 // through LDS for the transposing read. The eight waves of a block and the blocks of grid y take other token
 // blocks in turn, the next on its way under the current one; the waves' sums meet in LDS in order, the blocks'
-// in gemm16_join_kernel. (32 x 4096 from 4607 tokens, 20 MB: 8.6 + 2.7 us, where the product kernel took 16 + 5
+// in gemm16_join_kernel. (32 x 4096 from 4607 tokens, 20 MB: 9.8 + 3.9 us, where the product kernel took 16 + 5
 // with seven eighths of its rows empty; one round of blocks, bound by the latency of a few loads in a row.)
 constexpr int FG_WAVES = 8;
 template <int NT>   // 32-row tiles of dW
@@ -612,14 +613,14 @@ __global__ __launch_bounds__(64 * FG_WAVES, NT == 1 ? 4 : 2) void factor_grad_ke
     }
 }
 
-// ------------------------------------------------------------------- gated forward, 1 to 48 rows
+// ------------------------------------------------------------------- gated forward, 1 to 32 rows
 // Bound by reading the weights. A block takes 16 columns of H, its eight waves an eighth of the contraction
 // each (interleaved by 64, so the block reads whole lines of each weight row); X's operands (MT tiles of 16
 // rows) come straight from memory, where its few rows stay in the caches. The waves' sums meet in LDS, four
 // and four, in wave order. Lane (r = lane % 16, j = lane / 16) takes the contraction 64 i + 16 j + 0..15 of
-// weight row r and of X row r in two operands. (4096 x 12288: 1 row 43 us, 16 rows 50, 32 rows 59, where the
-// product kernel takes 80; with 32 columns a block 72 for 32 rows; at 64 rows both take 81 to 86.)
-constexpr int GT_WAVES = 8, GT_MAX_M = 48;
+// weight row r and of X row r in two operands. (4096 x 12288: 1 row 43 us, 16 rows 50, 17 rows 50, where the
+// product kernel takes 59, 32 rows 61 like that kernel, 48 rows 71 to its 62; 1024 x 2816: 32 rows 9.3 to 10.5.)
+constexpr int GT_WAVES = 8, GT_MAX_M = 32;
 template <int MT>
 __global__ __launch_bounds__(64 * GT_WAVES) void gated_token_kernel(const uint16_t* __restrict__ X, int M, int K, int ldx,
                                                                     const uint16_t* __restrict__ Wg,
@@ -805,10 +806,8 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
     const dim3 grid(tiles_of(F, 16)), block(64 * GT_WAVES);
     if (M <= 16)
       hipLaunchKernelGGL(gated_token_kernel<1>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
-    else if (M <= 32)
-      hipLaunchKernelGGL(gated_token_kernel<2>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
     else
-      hipLaunchKernelGGL(gated_token_kernel<3>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
+      hipLaunchKernelGGL(gated_token_kernel<2>, grid, block, 0, st, X, M, K, ldx, Wg, Wu, ldw, F, act, H, ldh);
     e = hipGetLastError();
   } else {
     GatedOperands o;
