@@ -550,6 +550,16 @@ def test_gated_backward(M, K, F, act):
 
 
 @gpu
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,K,F", [(227, 2240, 2312), (40, 4096, 136), (1000, 4096, 264), (33, 1024, 8)])
+def test_gated_long_contraction_in_parts(M, K, F, act):
+    """Few blocks of outputs over a long contraction: its parts are added before the activation."""
+    assert w4.gated_forward_bytes(M, K, F) >= 2 * 2 * M * F * 4
+    test_gated_forward(M, K, F, act)
+    test_gated_backward(M, K, F, act)
+
+
+@gpu
 def test_gated_saturated_and_non_finite():
     """Gates far outside the exponential's range, and rows with Inf or NaN that stay apart."""
     for M in (9, 40):

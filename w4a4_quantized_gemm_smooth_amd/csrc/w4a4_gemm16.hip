@@ -40,7 +40,7 @@ using namespace w4a4::dev;
 namespace {
 
 enum : int { ROWS = 0, COLS = 1, CODES = 2 };
-enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_GATED = 2, OUT_GATED_GRAD = 3 };
+enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_GATED = 2, OUT_GATED_GRAD = 3, OUT_GATED_F32 = 4 };   // F32: planes, or the result itself
 
 constexpr int TILE = 256, SMALL_TILE = 128;   // block rows and columns (gated: half as many columns)
 constexpr int KSTEP = 32;        // contraction per step
@@ -60,7 +60,7 @@ struct GemmArgs {
   int lda, ldb, ldo, lddh;
   int rows, cols, K;               // per problem; K per segment; gated: cols of one weight
   int segs, probs, steps;          // steps per segment
-  int splits;                      // parts of the contraction, each to its own plane of out[0] (OUT_F32)
+  int splits;                      // parts of the contraction, each to its own plane of out[0] (and of out[1], gated)
 };
 
 // COLS: the four rows that a transposing read takes for 16 lanes, and the two column halves beside them,
@@ -133,10 +133,11 @@ __device__ __forceinline__ void store_block(const v16f (&t)[MT][2], uint8_t* sta
 
 // As store_block, in fp32: 64 rows of 256 bytes at a time fill a wave's 16 KB, chunk c of row r at c ^ (r & 15)
 // (32 lanes write one chunk of 32 rows: other banks), and go out as whole rows. (Straight from the registers,
-// 128 bytes of a row at a time, the planes of 4096 x 512 x 5 took 24 us more.)
-template <int MT>
-__device__ __forceinline__ void store_block_f32(const v16f (&t)[MT][2], uint8_t* stage, float* out, int ld, int rows, int cols, int r0,
-                                                int c0, int lane) {
+// 128 bytes of a row at a time, the planes of 4096 x 512 x 5 took 24 us more.) PAIR: the two tiles are the same
+// columns of two results.
+template <bool PAIR, int MT>
+__device__ __forceinline__ void store_block_f32(const v16f (&t)[MT][2], uint8_t* stage, float* out, float* second, int ld, int rows,
+                                                int cols, int r0, int c0, int lane) {
   const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
   for (int half = 0; half < MT / 2; ++half) {
@@ -154,8 +155,8 @@ __device__ __forceinline__ void store_block_f32(const v16f (&t)[MT][2], uint8_t*
     for (int q = 0; q < 16; ++q) {
       const int rr = 4 * q + (lane >> 4), c = lane & 15;
       const float4 val = *reinterpret_cast<const float4*>(stage + rr * 256 + 16 * (c ^ (rr & 15)));
-      const int row = r0 + half * 64 + rr, col = c0 + 4 * c;
-      if (row < rows && col < cols) *reinterpret_cast<float4*>(out + (size_t)row * ld + col) = val;
+      const int row = r0 + half * 64 + rr, col = c0 + 4 * (PAIR ? c & 7 : c);
+      if (row < rows && col < cols) *reinterpret_cast<float4*>((PAIR && c >= 8 ? second : out) + (size_t)row * ld + col) = val;
     }
   }
 }
@@ -187,7 +188,7 @@ __device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, in
 // SMALL: blocks of 128 x 128, four waves of 64 x 64, two blocks to a compute unit; the same otherwise.
 template <int AM, int BM, int EPI, int ACT, bool SMALL>
 __global__ __launch_bounds__(SMALL ? 256 : 512, SMALL ? 2 : 1) void gemm16_kernel(const GemmArgs g) {
-  constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
+  constexpr bool GATED = EPI >= OUT_GATED;
   constexpr bool PERM = BM == CODES;   // contraction order of a step: 16 h + 8 s + e instead of 16 s + 8 h + e
   constexpr int W = SMALL ? SMALL_TILE : TILE, MT = SMALL ? 2 : 4, WN = W / 64;   // 32-row tiles of a wave, waves along N
   constexpr int NA = W / 64, NB = BM == CODES ? NA / 2 + 1 : NA, NDMA = NA + NB;   // copies per copying wave and step
@@ -429,8 +430,12 @@ __global__ __launch_bounds__(SMALL ? 256 : 512, SMALL ? 2 : 1) void gemm16_kerne
   if constexpr (EPI == OUT_BF16) {
     store_block<0, 2>(acc, stage, static_cast<uint16_t*>(g.out[prob]), g.ldo, g.rows, g.cols, r0, n0 + 64 * wn, lane);
   } else if constexpr (EPI == OUT_F32) {
-    store_block_f32(acc, stage, static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo, g.ldo, g.rows, g.cols, r0,
-                    n0 + 64 * wn, lane);
+    store_block_f32<false>(acc, stage, static_cast<float*>(g.out[prob]) + (size_t)blockIdx.y * g.rows * g.ldo, nullptr, g.ldo, g.rows,
+                           g.cols, r0, n0 + 64 * wn, lane);
+  } else if constexpr (EPI == OUT_GATED_F32) {
+    const size_t plane = (size_t)blockIdx.y * g.rows * g.ldo;
+    store_block_f32<true>(acc, stage, static_cast<float*>(g.out[0]) + plane, static_cast<float*>(g.out[1]) + plane, g.ldo, g.rows, g.cols,
+                          r0, n0 + 32 * wn, lane);
   } else {
     const int c0 = n0 + 32 * wn;
     if constexpr (EPI == OUT_GATED_GRAD) {   // dH's rows: 64 of them at a time, 5 KB
@@ -474,6 +479,7 @@ __global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restric
   part += blockIdx.y * splits * n;
   T* out = blockIdx.y ? out1 : out0;
   float4 s = *reinterpret_cast<const float4*>(part + i);
+#pragma unroll 8   // loads on their way together
   for (int q = 1; q < splits; ++q) {
     const float4 v = *reinterpret_cast<const float4*>(part + q * n + i);
     s.x += v.x;
@@ -485,6 +491,47 @@ __global__ __launch_bounds__(256) void gemm16_join_kernel(const float* __restric
     *reinterpret_cast<float4*>(out + i) = s;
   else
     *reinterpret_cast<uint2*>(out + i) = uint2{pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w)};
+}
+
+// The same for the gated products' planes (n = M F values each, the second product's after the first's), and
+// what the product kernel does with the sums: H, or dG and dU from dH.
+template <bool GRAD, int ACT>
+__global__ __launch_bounds__(256) void gated_join_kernel(const float* __restrict__ part, int splits, uint32_t n, int F,
+                                                         const uint16_t* __restrict__ dH, int lddh, uint16_t* __restrict__ out0,
+                                                         uint16_t* __restrict__ out1, int ldo) {
+  const uint32_t i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;   // F is a multiple of 8: four values of a row
+  const uint32_t row = i / (uint32_t)F, col = i - row * (uint32_t)F;
+  uint2 d = {0u, 0u};
+  if constexpr (GRAD) d = *reinterpret_cast<const uint2*>(dH + (size_t)row * lddh + col);
+  float4 s[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const float* p = part + (size_t)y * splits * n + i;
+    s[y] = *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
+    for (int q = 1; q < splits; ++q) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (size_t)q * n);
+      s[y].x += v.x;
+      s[y].y += v.y;
+      s[y].z += v.z;
+      s[y].w += v.w;
+    }
+  }
+  const float g[4] = {s[0].x, s[0].y, s[0].z, s[0].w}, u[4] = {s[1].x, s[1].y, s[1].z, s[1].w};
+  const float dh[4] = {__uint_as_float(d.x << 16), __uint_as_float(d.x & 0xFFFF0000u), __uint_as_float(d.y << 16),
+                       __uint_as_float(d.y & 0xFFFF0000u)};
+  float x[4], y[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    float a, slope;
+    act_of<ACT>(g[v], a, slope);
+    x[v] = GRAD ? dh[v] * u[v] * slope : a * u[v];
+    y[v] = dh[v] * a;
+  }
+  const size_t at = (size_t)row * ldo + col;
+  *reinterpret_cast<uint2*>(out0 + at) = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  if constexpr (GRAD) *reinterpret_cast<uint2*>(out1 + at) = uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
 // Rows that do not start at multiples of 64 bytes take the copies by ROWS twice the lines (2041 x 2056 x 5624,
@@ -690,7 +737,7 @@ inline int tiles_of(int n, int t) { return (n + t - 1) / t; }
 
 template <int AM, int BM, int EPI, int ACT = 0>
 hipError_t launch(const GemmArgs& g, bool small, hipStream_t st) {
-  constexpr bool GATED = EPI == OUT_GATED || EPI == OUT_GATED_GRAD;
+  constexpr bool GATED = EPI >= OUT_GATED;
   const int w = small ? SMALL_TILE : TILE;
   const long long blocks = (long long)tiles_of(g.rows, w) * g.probs * tiles_of(g.cols, GATED ? w / 2 : w);
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
@@ -712,10 +759,13 @@ hipError_t join(const float* part, int splits, long long n, T* out, hipStream_t 
 // added by the join; 0: it cannot be split), whichever a simple cost favours. Measured: a round of large blocks
 // (256) 0.6 us a step (0.9 at the chip's power limit: all blocks at length) and 8 us besides, of small ones
 // (512, two to a compute unit) 0.45 us (0.35 up to 256; with codes, which each wave converts for half as many
-// rows, 0.75 and 0.5) and 5 us; a plane's value, written and read, 8 bytes at 6 TB/s; 6 us for the join's launch.
+// rows, 0.75 and 0.5) and 5 us, but not less than the operands at 4.9 TB/s and 5 us; a plane's value, written and
+// read, 8 bytes at 6 TB/s; 8 us for the join's launch.
 // Parts are at least 4 steps long. Both sides (calls, us, large / small): gated forward 300 x 520 x 392 15.8 /
 // 9.7, 128 x 4096 x 12288 91 / 63, 2048 x 1024 x 4096 35 / 47; backward 1000 x 1024 x 2816 81 / 73, 2041 x 2056 x
-// 5624 334 / 398; weight gradient 200 x 8192 from 8192 tokens 53 / 67.
+// 5624 334 / 398; weight gradient 200 x 8192 from 8192 tokens 53 / 67. The gated products whole / in parts: 40 x
+// 4096 x 136 28 / 14, 64 x 4096 x 4096 40 / 22, 1000 x 4096 x 264 39 / 21; 128 x 4096 x 12288 63 / 71, 64 x 1024 x
+// 2816 10 / 12.
 struct Plan {
   bool small;
   int splits;
@@ -723,12 +773,14 @@ struct Plan {
 Plan plan_of(int rows, int probs, int cols, bool gated, bool codes, int steps, double values) {
   Plan best{false, 1};
   double least = 0.;
+  const double bytes = (double)steps * KSTEP * (2. * rows * probs + (gated ? 4. : codes ? 1. : 2.) * cols), floor = bytes / 4.9e6 + 5.;
   for (int small = 0; small < 2; ++small) {
     const int w = small ? SMALL_TILE : TILE, round = small ? 512 : 256;
     const long long blocks = (long long)tiles_of(rows, w) * probs * tiles_of(cols, gated ? w / 2 : w);
     for (int s = 1; s == 1 || (values > 0. && s <= steps / 4 && s <= 64 && blocks * s <= 2 * round); ++s) {
       const double rounds = (double)((blocks * s + round - 1) / round), step = !small ? 0.6 : blocks * s <= 256 ? (codes ? 0.5 : 0.35) : codes ? 0.75 : 0.45;
-      const double t = rounds * (step * ((steps + s - 1) / s) + (small ? 5. : 8.)) + (s > 1 ? 6. + s * values * 8. / 6e6 : 0.);
+      const double product = rounds * (step * ((steps + s - 1) / s) + (small ? 5. : 8.));
+      const double t = (product > floor ? product : floor) + (s > 1 ? 8. + s * values * 8. / 6e6 : 0.);
       if ((small == 0 && s == 1) || t < least) {
         least = t;
         best = Plan{small == 1, s};
@@ -744,8 +796,8 @@ bool gated_shape_ok(int M, int K, int F) {
 bool ld_ok(int ld, int cols) { return ld >= cols && ld % 8 == 0 && ld <= GM_MAX_LD; }
 
 // Workspace: for large products whose K is no multiple of 32, room for X, Wg and Wu with rows of a multiple of
-// 64 bytes; for the backward pass then dG, dU [M][F up to a multiple of 32] bf16, and the planes of a split
-// contraction (dX's, then the two weights').
+// 64 bytes; for the backward pass then dG, dU [M][F up to a multiple of 32] bf16; and the planes of a split
+// contraction (the two projections', then dX's, then the two weights').
 inline int pad32(int n) { return (n + 31) / 32 * 32; }
 size_t matrix_bytes(int rows, int cols) { return ((size_t)rows * pad32(cols) * 2 + 255) / 256 * 256; }
 // Only where the steps' extra time (measured: 0.35 us a step of a round of 256 blocks) clearly exceeds the copy's.
@@ -781,7 +833,33 @@ hipError_t gated_operands(const uint16_t* X, int M, int K, int ldx, const uint16
   hipLaunchKernelGGL(pad_rows_kernel, dim3(1024, 3), dim3(256), 0, st, a);
   return hipGetLastError();
 }
-Plan gated_plan(int M, int K, int F) { return plan_of(M, 1, F, true, false, tiles_of(K, KSTEP), 0.); }
+Plan gated_plan(int M, int K, int F) { return plan_of(M, 1, F, true, false, tiles_of(K, KSTEP), 2. * M * F); }
+size_t gated_plane_bytes(int M, int K, int F) {
+  const int s = gated_plan(M, K, F).splits;
+  return s > 1 ? (size_t)s * 2 * M * F * 4 : 0;
+}
+// Both projections of the operands, to H (grad false) or, with dH, to dG and dU.
+template <int ACT>
+hipError_t gated_products(const GatedOperands& o, int M, int K, int F, bool grad, const uint16_t* dH, int lddh, uint16_t* out0,
+                          uint16_t* out1, int ldo, float* planes, hipStream_t st) {
+  const Plan plan = gated_plan(M, K, F);
+  GemmArgs g{};
+  g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = out0, g.out[1] = out1, g.dH = dH;
+  g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldo, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
+  g.segs = g.probs = 1, g.splits = plan.splits, g.steps = tiles_of(K, KSTEP);
+  if (plan.splits == 1)
+    return grad ? launch<ROWS, ROWS, OUT_GATED_GRAD, ACT>(g, plan.small, st) : launch<ROWS, ROWS, OUT_GATED, ACT>(g, plan.small, st);
+  const size_t n = (size_t)M * F;   // split: at most 512 small or 256 large blocks a part, so below 2^31
+  g.out[0] = planes, g.out[1] = planes + plan.splits * n, g.ldo = F;
+  const hipError_t e = launch<ROWS, ROWS, OUT_GATED_F32>(g, plan.small, st);
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)((n / 4 + 255) / 256)), block(256);
+  if (grad)
+    hipLaunchKernelGGL((gated_join_kernel<true, ACT>), grid, block, 0, st, planes, plan.splits, (uint32_t)n, F, dH, lddh, out0, out1, ldo);
+  else
+    hipLaunchKernelGGL((gated_join_kernel<false, ACT>), grid, block, 0, st, planes, plan.splits, (uint32_t)n, F, dH, lddh, out0, out1, ldo);
+  return hipGetLastError();
+}
 Plan gated_dx_plan(int M, int K, int F) { return plan_of(M, 1, K, false, false, 2 * tiles_of(F, KSTEP), (double)M * K); }
 Plan gated_dw_plan(int M, int K, int F) { return plan_of(F, 2, K, false, false, tiles_of(M, KSTEP), 2. * F * K); }
 
@@ -791,7 +869,7 @@ Plan gated_dw_plan(int M, int K, int F) { return plan_of(F, 2, K, false, false, 
 extern "C" {
 
 size_t w4a4_gated_forward_bytes(int M, int K, int F) {
-  return gated_shape_ok(M, K, F) ? gated_pad_bytes(M, K, F) : 0;
+  return gated_shape_ok(M, K, F) && M > GT_MAX_M ? gated_pad_bytes(M, K, F) + gated_plane_bytes(M, K, F) : 0;
 }
 
 w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg, const uint16_t* Wu, int ldw,
@@ -799,7 +877,7 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
   if (act != W4A4_ACT_SILU && act != W4A4_ACT_GELU) return W4A4_ERR_UNSUPPORTED;
   if (!gated_shape_ok(M, K, F) || !ld_ok(ldx, K) || !ld_ok(ldw, K) || !ld_ok(ldh, F)) return W4A4_ERR_INVALID_ARG;
   if (!X || !Wg || !Wu || !H || !aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H)) return W4A4_ERR_INVALID_ARG;
-  if (gated_pad_bytes(M, K, F) > 0 && (!ws || !aligned16(ws))) return W4A4_ERR_INVALID_ARG;
+  if (w4a4_gated_forward_bytes(M, K, F) > 0 && (!ws || !aligned16(ws))) return W4A4_ERR_INVALID_ARG;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   hipError_t e;
   if (M <= GT_MAX_M) {
@@ -813,13 +891,9 @@ w4a4_status_t w4a4_gated_forward(const uint16_t* X, int M, int K, int ldx, const
     GatedOperands o;
     e = gated_operands(X, M, K, ldx, Wg, Wu, ldw, F, ws, o, st);
     if (e != hipSuccess) return W4A4_ERR_HIP;
-    GemmArgs g{};
-    g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = H;
-    g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldh, g.rows = M, g.cols = F, g.K = K;
-    g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
-    const bool small = gated_plan(M, K, F).small;
-    e = act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_SILU>(g, small, st)
-                             : launch<ROWS, ROWS, OUT_GATED, W4A4_ACT_GELU>(g, small, st);
+    float* planes = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + gated_pad_bytes(M, K, F));
+    e = act == W4A4_ACT_SILU ? gated_products<W4A4_ACT_SILU>(o, M, K, F, false, nullptr, 0, H, nullptr, ldh, planes, st)
+                             : gated_products<W4A4_ACT_GELU>(o, M, K, F, false, nullptr, 0, H, nullptr, ldh, planes, st);
   }
   return e == hipSuccess ? W4A4_OK : W4A4_ERR_HIP;
 }
@@ -828,7 +902,8 @@ size_t w4a4_gated_backward_bytes(int M, int K, int F) {
   if (!gated_shape_ok(M, K, F)) return 0;
   const int sx = gated_dx_plan(M, K, F).splits, sw = gated_dw_plan(M, K, F).splits;
   const size_t px = sx > 1 ? (size_t)sx * M * K * 4 : 0, pw = sw > 1 ? (size_t)sw * 2 * F * K * 4 : 0;
-  return gated_pad_bytes(M, K, F) + 2 * gated_hidden_bytes(M, F) + (px > pw ? px : pw);
+  const size_t pg = gated_plane_bytes(M, K, F), most = px > pw ? px : pw;
+  return gated_pad_bytes(M, K, F) + 2 * gated_hidden_bytes(M, F) + (pg > most ? pg : most);
 }
 
 w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* X, int M, int K, int ldx, const uint16_t* Wg,
@@ -849,13 +924,9 @@ w4a4_status_t w4a4_gated_backward(const uint16_t* dH, int lddh, const uint16_t* 
   GatedOperands o;
   if (gated_operands(X, M, K, ldx, Wg, Wu, ldw, F, ws, o, st) != hipSuccess) return W4A4_ERR_HIP;
 
-  GemmArgs g{};   // both projections again, then dG and dU rounded to bf16, the operands of what follows
-  g.A[0] = o.x, g.B[0] = o.wg, g.B[1] = o.wu, g.out[0] = dG, g.out[1] = dU, g.dH = dH;
-  g.lda = o.ldx, g.ldb = o.ldw, g.ldo = ldg, g.lddh = lddh, g.rows = M, g.cols = F, g.K = K;
-  g.segs = g.probs = g.splits = 1, g.steps = tiles_of(K, KSTEP);
-  const bool small = gated_plan(M, K, F).small;
-  if ((act == W4A4_ACT_SILU ? launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_SILU>(g, small, st)
-                            : launch<ROWS, ROWS, OUT_GATED_GRAD, W4A4_ACT_GELU>(g, small, st)) != hipSuccess)
+  // both projections again, then dG and dU rounded to bf16, the operands of what follows
+  if ((act == W4A4_ACT_SILU ? gated_products<W4A4_ACT_SILU>(o, M, K, F, true, dH, lddh, dG, dU, ldg, planes, st)
+                            : gated_products<W4A4_ACT_GELU>(o, M, K, F, true, dH, lddh, dG, dU, ldg, planes, st)) != hipSuccess)
     return W4A4_ERR_HIP;
 
   GemmArgs x{};   // dX = [dG dU] [Wg; Wu]
