@@ -25,11 +25,11 @@
 // sizes cost nothing in the loop. Results are computed transposed (B as the first operand), which leaves a
 // lane four neighbouring columns of a row.
 //
-// Measured: gated forward 4608 x 4096 x 12288 774 us = 1200 TFLOP/s (the library's product of the same size
+// Measured: gated forward 4608 x 4096 x 12288 772 us = 1200 TFLOP/s (the library's product of the same size
 // 1084, its 8192^3 1290), at 1.64 GHz with the matrix unit 68% busy: the chip's power sets the pace; weight
-// gradient 4096 x 12288 from 4608 tokens' codes 452 us = 1030 TFLOP/s (the library's products of transposed
+// gradient 4096 x 12288 from 4608 tokens' codes 450 us = 1030 TFLOP/s (the library's products of transposed
 // operands 1006 to 1089). Small grids are bound by rounds of blocks: gradients 2041 x 2056 x 5624 in 20
-// (rows laid out anew) + 118 + 92 + 10 + 88 us.
+// (rows laid out anew) + 121 + 96 + 10 + 95 us.
 #include <type_traits>
 
 #include "w4a4_device_common.h"
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const PadArgs a) {
 // token block's codes as the matrix operand needs them (16 of a channel's 32 tokens), and dY's 32 tokens go
 // through LDS for the transposing read. The eight waves of a block and the blocks of grid y take other token
 // blocks in turn, the next on its way under the current one; the waves' sums meet in LDS in order, the blocks'
-// in gemm16_join_kernel. (32 x 4096 from 4607 tokens, 20 MB: 9.8 + 3.9 us, where the product kernel took 16 + 5
+// in gemm16_join_kernel. (32 x 4096 from 4607 tokens, 20 MB: 8.7 + 2.8 us, where the product kernel took 16 + 5
 // with seven eighths of its rows empty; one round of blocks, bound by the latency of a few loads in a row.)
 constexpr int FG_WAVES = 8;
 template <int NT>   // 32-row tiles of dW

@@ -23,8 +23,8 @@
 // the slices in slice order, t L2 and the bias. Small layers (K <= 1024, L1 of at most 64 KB) are one kernel:
 // a block takes all of K, makes t for itself and finishes its rows.
 //
-// Measured: 1 x 9216 x 3072 INT4, rank 32 (15.9 MB): 7.1 + 3.2 us; 13 x 3072 x 12288, rank 48 (22 MB): 12.2 +
-// 3.9 us; 1 x 635 x 256: 4.6 us, one kernel. An empty launch takes 2.2 us and the bytes at the rate of a large
+// Measured: 1 x 9216 x 3072 INT4, rank 32 (15.9 MB): 6.9 + 3.3 us; 13 x 3072 x 12288, rank 48 (22 MB): 12.1 +
+// 4.1 us; 1 x 635 x 256: 4.6 us, one kernel. An empty launch takes 2.2 us and the bytes at the rate of a large
 // copy 3.2 and 4.5 us, so what is left is the ramp of one round of blocks (the same for 128 to 1024 blocks)
 // and, above 8 rows, the second matrix operand.
 #include "w4a4_device_common.h"
